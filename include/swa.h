@@ -316,6 +316,129 @@ int swa_hybrid_decode(const void* q, const void* k_new, const void* v_new, const
 int swa_hadamard_proj(const void* y, const float* alpha, const float* beta, void* z,
                       long long n_rows, int n, int out_dtype, swa_stream_t stream);
 
+/*
+ * 4-bit ring cache: the ring cache above with rows in 4 bits ("Sliding-window beats
+ * linear attention", section 1: the fixed memory of sliding-window attention at
+ * inference, here 80 bytes a row instead of 256 at d = 128).  The pages have no
+ * quantised cache; definition used, by groups of 32 neighbouring elements of a row:
+ *     lo = min,  step = bf16((max - lo) * (1/15)), 0 where that is below 2^-126,
+ *     code = rint((x - lo) * (1/step)) clamped to 0..15,  value = code * step + lo,
+ * each operation rounded to float32 (step to bf16; rint to even), so that the codes
+ * are reproducible bit for bit.  Elements must be finite with |x| <= 2^126; a group
+ * that holds another value stands for unspecified ones, and no other group does.
+ * Layout (bytes, 16-byte aligned base):
+ *     kcache, vcache  [B, Hkv, window, swa_kv4_row_bytes(d)]   slots as in swa_cache_fill
+ *     sink_k, sink_v  [B, Hkv, n_sink, swa_kv4_row_bytes(d)]
+ * A row is d/2 bytes of codes, then d/32 pairs (step, lo) in bf16.  Two codes share a
+ * byte, the earlier one in the low nibble; seen as [d/32, 8, 4] the elements are
+ * stored in the order [8, d/32, 4].
+ * Supported: d in {64, 128} (swa_kv4_row_bytes is 0 otherwise).
+ *
+ * swa_kv4_cache_fill, swa_kv4_cache_append: as swa_cache_fill and swa_cache_append,
+ *   with the rows of k, v (bf16) quantised as they are written.  A negative pos[b]
+ *   leaves sequence b as it is.
+ * swa_kv4_cache_read: the values of cached positions, positions DEVICE int32 [B, n]:
+ *   k_out, v_out [B, n, Hkv, d] (out_dtype SWA_DTYPE_BF16 or SWA_DTYPE_F32).  Position
+ *   p < n_sink is read from sink slot p, any other from ring slot p mod window; p < 0
+ *   gives zeros.  The caller asks for positions that the cache holds.
+ * swa_kv4_decode: as swa_decode_ex (out_dtype SWA_DTYPE_BF16 or SWA_DTYPE_BF16_F32OUT)
+ *   over the 4-bit cache.  It needs no workspace, so that any number of calls may run
+ *   at once.  A sequence with pos[b] < 0 has no keys: out = 0, lse = -inf.  Scores and
+ *   sums are float32; the softmax numerators, times a group's step, are rounded to 11
+ *   significant bits.  Supported: Hq / Hkv <= 8, |q| < 2^100, step < 2^100.
+ */
+size_t swa_kv4_row_bytes(int d);
+int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* vcache, void* sink_k, void* sink_v,
+                       int B, int Hkv, int d, int window, int n_sink, swa_stream_t stream);
+int swa_kv4_cache_append(const void* k_new, const void* v_new, const int32_t* pos, void* kcache, void* vcache,
+                         void* sink_k, void* sink_v, int B, int Hkv, int d, int window, int n_sink,
+                         swa_stream_t stream);
+int swa_kv4_cache_read(const int32_t* positions, int n, const void* kcache, const void* vcache, const void* sink_k,
+                       const void* sink_v, void* k_out, void* v_out, int out_dtype, int B, int Hkv, int d, int window,
+                       int n_sink, swa_stream_t stream);
+int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const void* sink_k, const void* sink_v,
+                   const int32_t* pos, void* out, float* lse, int B, int Hq, int Hkv, int d, int window, int n_sink,
+                   float scale, int out_dtype, swa_stream_t stream);
+
+/*
+ * Cache of a fixed capacity that evicts by accumulated attention weight: where the
+ * ring cache keeps the last `window` positions, this one keeps the positions that the
+ * queries have used.  The sinks ("Sliding-window beats linear attention", section 3:
+ * the first tokens must be kept) and the `recent` last positions always stay.  The
+ * pages have no such cache; definition used below.  Layout:
+ *     kcache, vcache [B, Hkv, capacity, d] bf16,  slots in any order
+ *     slot_pos       [B, Hkv, capacity] int32     position in the slot, < 0: empty
+ *     score          [B, Hkv, capacity] float32   weight the slot has accumulated
+ * An empty cache is slot_pos filled with -1 and score with 0.
+ * Requires n_sink >= 0, recent >= 1, capacity >= n_sink + recent.
+ * Supported: d in {64, 128}, capacity <= 16384.
+ *
+ * swa_hh_scores: the weight each key of a prompt received from the last n_obs queries,
+ *     score[b, h, j] = sum over t in [L - n_obs, L), query heads g of KV head h, with
+ *                      j visible to t:  exp(scale q_t,g . k_j,h - lse[b, g, t]);
+ *   q [B, L, Hq, d], k [B, L, Hkv, d] bf16, lse [B, Hq, L] float32 as swa_fwd takes and
+ *   leaves them (window and n_sink as given there; window >= L for full causal
+ *   attention), score [B, Hkv, L] float32 (written whole).  0 <= n_obs <= L.
+ * swa_hh_cache_fill: keeps positions of a prompt k, v [B, L, Hkv, d] bf16 given
+ *   score_in [B, Hkv, L] float32: all where L <= capacity; else the first n_sink, the
+ *   last `recent`, and of the others those with the largest score (of equal ones the
+ *   earlier) until the cache is full.  They are written in ascending order to slots
+ *   0, 1, ... with their score; slots behind them become empty (slot_pos -1, score 0;
+ *   their rows keep what they held).  A NaN counts as the lowest score.
+ * swa_hh_cache_append: writes k_new, v_new [B, Hkv, d] bf16 of position pos[b] (DEVICE
+ *   int32 [B]) into one slot of each (b, KV head), with score 0: the slot that holds
+ *   this position already; else an empty one; else of those with
+ *   n_sink <= slot_pos <= pos - recent the one with the lowest score; else (positions
+ *   not appended in order) the one with the lowest score.  Of equals the first slot; a
+ *   NaN counts as the lowest score.  slot [B, Hkv] int32 (may be NULL) receives the
+ *   slot.  A negative pos[b] leaves sequence b as it is and gives slot -1.
+ * swa_hh_decode: q [B, Hq, d] bf16 attends to the occupied slots (out [B, Hq, d] bf16,
+ *   or float32 by out_dtype SWA_DTYPE_BF16_F32OUT; lse [B, Hq] float32, may be NULL),
+ *   and each occupied slot's score becomes
+ *       decay * score + sum over the query heads of the KV head of its softmax weight.
+ *   0 <= decay <= 1.  Without occupied slots out = 0, lse = -inf.  Supported:
+ *   Hq / Hkv <= 8.  No workspace is needed, so that calls on different caches may run
+ *   at once.
+ */
+int swa_hh_scores(const void* q, const void* k, const float* lse, float* score, int B, int Hq, int Hkv, int L, int d,
+                  int n_obs, int window, int n_sink, float scale, swa_stream_t stream);
+int swa_hh_cache_fill(const void* k, const void* v, const float* score_in, int L, void* kcache, void* vcache,
+                      int32_t* slot_pos, float* score, int B, int Hkv, int d, int capacity, int n_sink, int recent,
+                      swa_stream_t stream);
+int swa_hh_cache_append(const void* k_new, const void* v_new, const int32_t* pos, void* kcache, void* vcache,
+                        int32_t* slot_pos, float* score, int32_t* slot, int B, int Hkv, int d, int capacity,
+                        int n_sink, int recent, swa_stream_t stream);
+int swa_hh_decode(const void* q, const void* kcache, const void* vcache, const int32_t* slot_pos, float* score,
+                  void* out, float* lse, int B, int Hq, int Hkv, int d, int capacity, float scale, float decay,
+                  int out_dtype, swa_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...) for tokens that lie on
+ * a grid, beside swa_rope_qk's one axis: each pair (x[i], x[i + d/2]), i < d/2, turns
+ * by positions[axis(i)][t] * theta_i.  sections[a] (HOST int32 [n_axes]) is the number
+ * of pairs of axis a; their sum is d/2.  layout:
+ *   SWA_ROPE_SECTIONS     the pairs of an axis are neighbours, in the order of the axes,
+ *                         theta_i = rope_base^(-2i/d)
+ *   SWA_ROPE_PER_AXIS     neighbours as well, each axis with frequencies of its own:
+ *                         theta = rope_base^(-m / sections[a]) for its m-th pair
+ *   SWA_ROPE_INTERLEAVED  pair i belongs to axis a = i mod n_axes if a > 0 and
+ *                         i / n_axes < sections[a], else to axis 0; theta as SECTIONS.
+ *                         The last pair of an axis a > 0, a + n_axes (sections[a] - 1),
+ *                         must be below d/2.
+ * q [n_tokens, Hq, d] and k [n_tokens, Hkv, d] (k may be NULL, or Hq = 0) are rotated in
+ * place; dtype SWA_DTYPE_BF16 or SWA_DTYPE_F32 (both alike).  q_stride and k_stride are
+ * the elements from one token to the next (Hq * d and Hkv * d when contiguous; at least
+ * that, and a multiple of 16 bytes), so that q and k may lie in one projection's
+ * output.  positions DEVICE int32 [n_axes, n_tokens].  inverse != 0 turns by the
+ * negative angles, which is also the backward pass: the gradient of a rotation is the
+ * inverse rotation of the gradient (swa_bwd's float32 dq, dk).  Angles as in
+ * swa_rope_qk.  Supported: d in {64, 128}, 1 <= n_axes <= 4.
+ */
+typedef enum { SWA_ROPE_SECTIONS = 0, SWA_ROPE_PER_AXIS = 1, SWA_ROPE_INTERLEAVED = 2 } swa_rope_layout;
+int swa_rope_axes_qk(void* q, void* k, const int32_t* positions, long long n_tokens, int Hq, int Hkv, int d,
+                     long long q_stride, long long k_stride, const int32_t* sections, int n_axes, int layout,
+                     double rope_base, int inverse, int dtype, swa_stream_t stream);
+
 /* Static text for a status code. */
 const char* swa_status_string(int status);
 

@@ -402,3 +402,128 @@ def based_linear_decode(q, k, v, S, z, scale: float):
     z = _f64(z) + fk
     out = np.einsum("bhf,bhfc->bhc", fq, S) / np.einsum("bhf,bhf->bh", fq, z)[..., None]
     return out, S, z
+
+
+# ---------------------------------------------------------------- 4-bit ring cache
+def kv4_quantise(x):
+    """Rows [..., d] by groups of 32: integer codes [..., d], and step and lo [..., d/32] as float64.
+    Each operation of the definition rounds to float32 (step to bf16), which numpy's float32
+    arithmetic does; what is returned is exact."""
+    import torch
+    r = _f64(x).astype(np.float32)
+    r = r.reshape(*r.shape[:-1], r.shape[-1] // 32, 32)
+    lo, hi = r.min(-1), r.max(-1)
+    raw = (hi - lo) * np.float32(1.0 / 15.0)
+    step = torch.from_numpy(np.ascontiguousarray(raw)).bfloat16().float().numpy()
+    step = np.where(step >= np.float32(2.0 ** -126), step, np.float32(0))
+    inv = np.zeros_like(step)
+    np.divide(np.float32(1), step, out=inv, where=step > 0)
+    code = np.clip(np.rint((r - lo[..., None]) * inv[..., None]), 0, 15)
+    return (code.reshape(_f64(x).shape).astype(np.int64), step.astype(np.float64), lo.astype(np.float64))
+
+
+def kv4_values(x) -> np.ndarray:
+    """The values that rows [..., d] stand for once they are in 4 bits."""
+    code, step, lo = kv4_quantise(x)
+    return code * np.repeat(step, 32, -1) + np.repeat(lo, 32, -1)
+
+
+def kv4_pack(x) -> np.ndarray:
+    """Rows [..., d] as bytes: d/2 of codes (elements seen as [d/32, 8, 4] in the order [8, d/32, 4],
+    low nibble first), then (step, lo) of each group in bf16."""
+    code, step, lo = kv4_quantise(x)
+    d = code.shape[-1]
+    out = np.zeros((*code.shape[:-1], d // 2 + d // 8), dtype=np.uint8)
+    for n in range(d):
+        j, g, i = n // 32, n % 32 // 4, n % 4
+        nib = (g * (d // 32) + j) * 4 + i
+        out[..., nib // 2] |= (code[..., n] << (4 * (nib % 2))).astype(np.uint8)
+    par = np.stack([step, lo], -1).astype(np.float32)
+    bits = (np.ascontiguousarray(par).view(np.uint32) >> 16).astype("<u2")  # exact: both are bf16 values
+    out[..., d // 2:] = np.ascontiguousarray(bits.reshape(*bits.shape[:-2], d // 16)).view(np.uint8)
+    return out
+
+
+# ---------------------------------------------------------------- eviction by weight
+def hh_scores(q, k, n_obs: int, window: int, n_sink: int, scale: float) -> np.ndarray:
+    """Weight each key of one prompt received from the last n_obs queries: q [B, L, Hq, d],
+    k [B, L, Hkv, d] -> [B, Hkv, L]."""
+    q, k = _f64(q), _f64(k)
+    B, L, Hq, _ = q.shape
+    Hkv = k.shape[2]
+    seen = visible_mask(L, window, n_sink)
+    out = np.zeros((B, Hkv, L))
+    for b in range(B):
+        for h in range(Hq):
+            z = np.where(seen, scale * q[b, :, h] @ k[b, :, h // (Hq // Hkv)].T, -np.inf)[L - n_obs:]
+            w = np.exp(z - z.max(1, keepdims=True)) if n_obs else z
+            out[b, h // (Hq // Hkv)] += (w / w.sum(1, keepdims=True)).sum(0) if n_obs else 0.0
+    return out
+
+
+def _hh_order(s) -> float:
+    """Sort key of a score: a NaN is the lowest, and -0 is 0."""
+    return -np.inf if s != s else float(s) + 0.0
+
+
+def hh_select(score, capacity: int, n_sink: int, recent: int) -> list:
+    """Positions of one prompt (score [L]) that a cache of this capacity keeps, ascending."""
+    L = len(score)
+    if L <= capacity:
+        return list(range(L))
+    always = [j for j in range(L) if j < n_sink or j >= L - recent]
+    rest = [j for j in range(n_sink, L - recent)]
+    nan_last = sorted(rest, key=lambda j: (-_hh_order(score[j]), score[j] != score[j], j))
+    return sorted(always + nan_last[:capacity - len(always)])
+
+
+def hh_victim(slot_pos, score, pos: int, n_sink: int, recent: int) -> int:
+    """The slot that position pos goes to: one (b, KV head), slot_pos and score [capacity]."""
+    n = len(slot_pos)
+    same = [i for i in range(n) if slot_pos[i] == pos]
+    empty = [i for i in range(n) if slot_pos[i] < 0]
+    may = [i for i in range(n) if n_sink <= slot_pos[i] <= pos - recent]
+    if same or empty:
+        return (same or empty)[0]
+    return min(may or range(n), key=lambda i: (_hh_order(score[i]), score[i] == score[i], i))
+
+
+def hh_decode(q, kcache, vcache, slot_pos, score, scale: float, decay: float = 1.0):
+    """One decode step over the occupied slots: out [B, Hq, d], lse [B, Hq] and the new scores."""
+    q, kc, vc = _f64(q), _f64(kcache), _f64(vcache)
+    B, Hq, d = q.shape
+    Hkv = kc.shape[1]
+    out, lse = np.zeros((B, Hq, d)), np.full((B, Hq), -np.inf)
+    new = _f64(score).copy()
+    for b in range(B):
+        for h in range(Hkv):
+            at = np.flatnonzero(np.asarray(slot_pos[b][h]) >= 0)
+            if not at.size:
+                continue
+            new[b, h, at] *= decay
+            for g in range(h * (Hq // Hkv), (h + 1) * (Hq // Hkv)):
+                z = scale * kc[b, h, at] @ q[b, g]
+                e = np.exp(z - z.max())
+                out[b, g] = e @ vc[b, h, at] / e.sum()
+                lse[b, g] = z.max() + np.log(e.sum())
+                new[b, h, at] += e / e.sum()
+    return out, lse, new
+
+
+# ---------------------------------------------------------------- rotary positions with axes
+def rope_axes(x, positions, sections, layout: str, base: float = 10000.0, inverse: bool = False) -> np.ndarray:
+    """Rotate x [T, H, d] by positions [n_axes, T]: complex multiplication of the pairs (i, i + d/2)."""
+    x = _f64(x)
+    half, n = x.shape[-1] // 2, len(sections)
+    y = x[..., :half] + 1j * x[..., half:]
+    first = np.concatenate([[0], np.cumsum(sections)])
+    for i in range(half):
+        if layout == "interleaved":
+            a = i % n if i % n and i // n < sections[i % n] else 0
+            theta = base ** (-i / half)
+        else:
+            a = int(np.searchsorted(first, i, side="right")) - 1
+            theta = base ** (-(i - first[a]) / sections[a]) if layout == "per_axis" else base ** (-i / half)
+        angle = np.asarray(positions[a], dtype=np.float64) * theta
+        y[..., i] *= np.exp((-1j if inverse else 1j) * angle)[:, None]
+    return np.concatenate([y.real, y.imag], -1)

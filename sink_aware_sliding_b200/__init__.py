@@ -11,6 +11,8 @@ streams).  Layouts follow ``swa.h``:
     varlen       q [T, Hq, d], k/v [T, Hkv, d], cu_seqlens int32 [n+1], lse [Hq, T]
     ring cache   kcache/vcache [B, Hkv, window, d], sink_k/sink_v [B, Hkv, n_sink, d]
     decode       q [B, Hq, d], pos int32 [B], out [B, Hq, d], lse [B, Hq]
+    4-bit cache  as the ring cache, uint8, swa_kv4_row_bytes(d) bytes in the place of d elements
+    hh cache     kcache/vcache [B, Hkv, capacity, d], slot_pos int32 / score float32 [B, Hkv, capacity]
 """
 from __future__ import annotations
 
@@ -39,7 +41,15 @@ EXPORTS = (
     "swa_hadamard_proj", "swa_rope_qk", "swa_rope_cache_append", "swa_decode_rope", "swa_bwd",
     "swa_based_linear_state_features", "swa_based_linear_fwd", "swa_based_linear_decode",
     "swa_decode_ex", "swa_debug_error_word", "swa_hybrid_decode",
+    "swa_kv4_row_bytes", "swa_kv4_cache_fill", "swa_kv4_cache_append", "swa_kv4_cache_read", "swa_kv4_decode",
+    "swa_hh_scores", "swa_hh_cache_fill", "swa_hh_cache_append", "swa_hh_decode", "swa_rope_axes_qk",
 )
+
+# Pair layouts of swa_rope_axes_qk.
+SWA_ROPE_SECTIONS = 0
+SWA_ROPE_PER_AXIS = 1
+SWA_ROPE_INTERLEAVED = 2
+_ROPE_LAYOUTS = {"sections": SWA_ROPE_SECTIONS, "per_axis": SWA_ROPE_PER_AXIS, "interleaved": SWA_ROPE_INTERLEAVED}
 
 _lib = None
 
@@ -78,6 +88,17 @@ def _load():
     lib.swa_based_linear_state_features.argtypes = [I]
     lib.swa_based_linear_fwd.argtypes = [P, P, P, P, P, P, I, I, I, I, I, F, I, P]
     lib.swa_based_linear_decode.argtypes = [P, P, P, P, P, P, I, I, I, I, F, I, P]
+    lib.swa_kv4_row_bytes.argtypes = [I]
+    lib.swa_kv4_row_bytes.restype = SZ
+    lib.swa_kv4_cache_fill.argtypes = [P, P, I, P, P, P, P, I, I, I, I, I, P]
+    lib.swa_kv4_cache_append.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P]
+    lib.swa_kv4_cache_read.argtypes = [P, I, P, P, P, P, P, P, I, I, I, I, I, I, P]
+    lib.swa_kv4_decode.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, P]
+    lib.swa_hh_scores.argtypes = [P, P, P, P, I, I, I, I, I, I, I, I, F, P]
+    lib.swa_hh_cache_fill.argtypes = [P, P, P, I, P, P, P, P, I, I, I, I, I, I, P]
+    lib.swa_hh_cache_append.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P]
+    lib.swa_hh_decode.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, F, I, P]
+    lib.swa_rope_axes_qk.argtypes = [P, P, P, LL, I, I, I, LL, LL, P, I, I, D, I, I, P]
     lib.swa_status_string.argtypes = [I]
     lib.swa_status_string.restype = ctypes.c_char_p
     lib.swa_device_error.argtypes = [P]
@@ -88,7 +109,9 @@ def _load():
     for name in ("swa_fwd", "swa_fwd_varlen", "swa_cache_fill", "swa_cache_append", "swa_decode",
                  "swa_decode_ex", "swa_debug_error_word", "swa_decode_noalloc", "swa_hybrid_decode", "swa_hadamard_proj", "swa_rope_qk", "swa_rope_cache_append",
                  "swa_decode_rope", "swa_bwd", "swa_based_linear_state_features", "swa_based_linear_fwd",
-                 "swa_based_linear_decode",
+                 "swa_based_linear_decode", "swa_kv4_cache_fill", "swa_kv4_cache_append", "swa_kv4_cache_read",
+                 "swa_kv4_decode", "swa_hh_scores", "swa_hh_cache_fill", "swa_hh_cache_append", "swa_hh_decode",
+                 "swa_rope_axes_qk",
                  "swa_device_error", "swa_set_debug_flags", "swa_version"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -360,6 +383,190 @@ def swa_hybrid_decode(q, k_new, v_new, pos, kcache, vcache, sink_k, sink_v, out,
                                    ctypes.c_float(scale_l if scale_l is not None else 1.0 / math.sqrt(dk)),
                                    _stream(stream))
     _check(st, "swa_hybrid_decode")
+
+
+def swa_kv4_row_bytes(d: int) -> int:
+    """Bytes of one row (one token, one KV head) of the 4-bit cache; 0 where d is not supported."""
+    return int(_load().swa_kv4_row_bytes(int(d)))
+
+
+def _gpu(t, name: str, dtype, shape) -> int:
+    """The address of a contiguous CUDA tensor on the current device, of this type and shape."""
+    import torch
+    _need(t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous(),
+          f"{name}: contiguous CUDA tensor, {dtype}, {list(shape)}")
+    _need(t.get_device() == torch.cuda.current_device(), f"{name}: on the current device")
+    return t.data_ptr()
+
+
+def _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
+    import torch
+    row = d // 2 + d // 8
+    ring, sink = (B, Hkv, window, row), (B, Hkv, n_sink, row)
+    addr = [_gpu(kcache, "kcache", torch.uint8, ring), _gpu(vcache, "vcache", torch.uint8, ring), None, None]
+    if n_sink > 0:
+        addr[2:] = _gpu(sink_k, "sink_k", torch.uint8, sink), _gpu(sink_v, "sink_v", torch.uint8, sink)
+    return addr
+
+
+def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink: int, stream=None) -> None:
+    """Quantise prefix positions 0..P-1 of k/v [B, P, Hkv, d] (bf16) into an empty 4-bit ring cache:
+    kcache/vcache [B, Hkv, window, row] uint8, sink_k/sink_v [B, Hkv, n_sink, row] (None without sinks)."""
+    import torch
+    _need(k.dim() == 4, "k [B, P, Hkv, d]")
+    B, P, Hkv, d = k.shape
+    kp, vp = _gpu(k, "k", torch.bfloat16, k.shape), _gpu(v, "v", torch.bfloat16, k.shape)
+    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, _stream(stream))
+    _check(st, "swa_kv4_cache_fill")
+
+
+def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, window: int, n_sink: int,
+                         stream=None) -> None:
+    """Quantise k_new/v_new [B, Hkv, d] (bf16) of positions pos (int32 [B]) into the 4-bit ring cache."""
+    import torch
+    _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
+    B, Hkv, d = k_new.shape
+    kp, vp = _gpu(k_new, "k_new", torch.bfloat16, k_new.shape), _gpu(v_new, "v_new", torch.bfloat16, k_new.shape)
+    pp = _gpu(pos, "pos", torch.int32, (B,))
+    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, _stream(stream))
+    _check(st, "swa_kv4_cache_append")
+
+
+def swa_kv4_cache_read(positions, kcache, vcache, sink_k, sink_v, k_out, v_out, window: int, n_sink: int,
+                       stream=None) -> None:
+    """The values of cached positions (int32 [B, n]) into k_out/v_out [B, n, Hkv, d] (both bf16 or both float32)."""
+    import torch
+    _need(k_out.dim() == 4 and k_out.dtype in (torch.bfloat16, torch.float32), "k_out [B, n, Hkv, d] bf16 or float32")
+    B, n, Hkv, d = k_out.shape
+    ko, vo = _gpu(k_out, "k_out", k_out.dtype, k_out.shape), _gpu(v_out, "v_out", k_out.dtype, k_out.shape)
+    pp = _gpu(positions, "positions", torch.int32, (B, n))
+    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    code = SWA_DTYPE_F32 if k_out.dtype == torch.float32 else SWA_DTYPE_BF16
+    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, _stream(stream))
+    _check(st, "swa_kv4_cache_read")
+
+
+def _decode_io(q, out, lse):
+    import torch
+    _need(q.dim() == 3 and out.dtype in (torch.bfloat16, torch.float32), "q [B, Hq, d], out bf16 or float32")
+    return (_gpu(q, "q", torch.bfloat16, q.shape), _gpu(out, "out", out.dtype, q.shape),
+            None if lse is None else _gpu(lse, "lse", torch.float32, q.shape[:2]),
+            SWA_DTYPE_BF16_F32OUT if out.dtype == torch.float32 else SWA_DTYPE_BF16)
+
+
+def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int, n_sink: int, scale=None,
+                   stream=None) -> None:
+    """One decode step over the 4-bit ring cache; q [B, Hq, d] bf16 at positions pos (int32 [B]);
+    writes out [B, Hq, d] (bf16 or float32) and lse [B, Hq] (or None).  No workspace."""
+    import torch
+    qp, op, lp, code = _decode_io(q, out, lse)
+    B, Hq, d = q.shape
+    _need(kcache.dim() == 4, "kcache [B, Hkv, window, row]")
+    Hkv = kcache.shape[1]
+    pp = _gpu(pos, "pos", torch.int32, (B,))
+    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_decode(qp, *cache, pp, op, lp, B, Hq, Hkv, d, window, n_sink, _scale(scale, d), code,
+                                _stream(stream))
+    _check(st, "swa_kv4_decode")
+
+
+def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=None, stream=None) -> None:
+    """Attention weight each key of a prompt received from the last n_obs queries: q [B, L, Hq, d],
+    k [B, L, Hkv, d] bf16 and lse [B, Hq, L] as swa_fwd takes and leaves them; writes score [B, Hkv, L] float32."""
+    import torch
+    _need(q.dim() == 4 and k.dim() == 4, "q [B, L, Hq, d], k [B, L, Hkv, d]")
+    B, L, Hq, d = q.shape
+    Hkv = k.shape[2]
+    st = _load().swa_hh_scores(_gpu(q, "q", torch.bfloat16, q.shape), _gpu(k, "k", torch.bfloat16, (B, L, Hkv, d)),
+                               _gpu(lse, "lse", torch.float32, (B, Hq, L)),
+                               _gpu(score, "score", torch.float32, (B, Hkv, L)), B, Hq, Hkv, L, d, n_obs, window,
+                               n_sink, _scale(scale, d), _stream(stream))
+    _check(st, "swa_hh_scores")
+
+
+def _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d):
+    import torch
+    _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
+    C = kcache.shape[2]
+    return C, (_gpu(kcache, "kcache", torch.bfloat16, (B, Hkv, C, d)),
+               _gpu(vcache, "vcache", torch.bfloat16, (B, Hkv, C, d)),
+               _gpu(slot_pos, "slot_pos", torch.int32, (B, Hkv, C)), _gpu(score, "score", torch.float32, (B, Hkv, C)))
+
+
+def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: int, recent: int, stream=None) -> None:
+    """Keep the first n_sink, the last `recent` and the heaviest other positions of a prompt k/v
+    [B, L, Hkv, d] (bf16), weights score_in [B, Hkv, L], in a cache of capacity kcache.shape[2]."""
+    import torch
+    _need(k.dim() == 4, "k [B, L, Hkv, d]")
+    B, L, Hkv, d = k.shape
+    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_fill(_gpu(k, "k", torch.bfloat16, k.shape), _gpu(v, "v", torch.bfloat16, k.shape),
+                                   _gpu(score_in, "score_in", torch.float32, (B, Hkv, L)), L, *cache, B, Hkv, d, C,
+                                   n_sink, recent, _stream(stream))
+    _check(st, "swa_hh_cache_fill")
+
+
+def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot, n_sink: int, recent: int,
+                        stream=None) -> None:
+    """Write k_new/v_new [B, Hkv, d] (bf16) of positions pos (int32 [B]) into the slot of that position,
+    an empty slot, or the lightest slot that may be evicted; slot int32 [B, Hkv] (or None) receives which."""
+    import torch
+    _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
+    B, Hkv, d = k_new.shape
+    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_append(_gpu(k_new, "k_new", torch.bfloat16, k_new.shape),
+                                     _gpu(v_new, "v_new", torch.bfloat16, k_new.shape),
+                                     _gpu(pos, "pos", torch.int32, (B,)), *cache,
+                                     None if slot is None else _gpu(slot, "slot", torch.int32, (B, Hkv)), B, Hkv, d, C,
+                                     n_sink, recent, _stream(stream))
+    _check(st, "swa_hh_cache_append")
+
+
+def swa_hh_decode(q, kcache, vcache, slot_pos, score, out, lse, scale=None, decay: float = 1.0, stream=None) -> None:
+    """One decode step over the occupied slots; q [B, Hq, d] bf16; writes out [B, Hq, d] (bf16 or float32)
+    and lse [B, Hq] (or None), and sets score = decay * score + the slot's softmax weights."""
+    qp, op, lp, code = _decode_io(q, out, lse)
+    B, Hq, d = q.shape
+    _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
+    Hkv = kcache.shape[1]
+    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), float(decay), code,
+                               _stream(stream))
+    _check(st, "swa_hh_decode")
+
+
+def _rope_rows(t, name: str, T: int, d: int):
+    """Address, heads and token stride of t [T, H, d]; its heads lie contiguously, its tokens may be apart."""
+    import torch
+    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(), f"{name}: CUDA tensor on the current device")
+    _need(t.dim() == 3 and t.shape[0] == T and t.shape[2] == d and t.stride(2) == 1 and t.stride(1) == d,
+          f"{name} [T, H, d] with contiguous heads")
+    return t.data_ptr(), t.shape[1], t.stride(0) if T > 1 else t.shape[1] * d
+
+
+def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_base: float = 10000.0,
+                     inverse: bool = False, stream=None) -> None:
+    """Rotate q [T, Hq, d] and k [T, Hkv, d] (k may be None; bf16 or float32) in place by positions of several
+    axes (int32 [n_axes, T]); sections: pairs of each axis, their sum d/2; layout "sections", "per_axis" or
+    "interleaved".  The tokens of q and k may be strided views.  inverse=True turns back (the backward pass)."""
+    import torch
+    _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float32), "q [T, Hq, d] bf16 or float32")
+    _need(layout in _ROPE_LAYOUTS, f"layout one of {sorted(_ROPE_LAYOUTS)}")
+    T, _, d = q.shape
+    qp, Hq, qs = _rope_rows(q, "q", T, d)
+    kp, Hkv, ks = None, 0, 0
+    if k is not None:
+        _need(k.dtype == q.dtype, "k of q's type")
+        kp, Hkv, ks = _rope_rows(k, "k", T, d)
+    n_axes = len(sections)
+    pp = _gpu(positions, "positions", torch.int32, (n_axes, T))
+    sec = (ctypes.c_int32 * max(1, n_axes))(*sections)
+    st = _load().swa_rope_axes_qk(qp, kp, pp, T, Hq, Hkv, d, qs, ks, sec, n_axes, _ROPE_LAYOUTS[layout],
+                                  float(rope_base), int(bool(inverse)),
+                                  SWA_DTYPE_F32 if q.dtype == torch.float32 else SWA_DTYPE_BF16, _stream(stream))
+    _check(st, "swa_rope_axes_qk")
 
 
 def swa_hadamard_proj(y, alpha, beta, z, stream=None) -> None:

@@ -1,0 +1,74 @@
+// Launch interfaces of the fixed-memory caches: the 4-bit ring cache, the cache
+// that evicts by accumulated attention weight, and rotary positions with axes.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace swa {
+
+// ---------------------------------------------------------------- 4-bit ring cache
+constexpr int kKv4Group = 32;  // elements that share a step and a minimum
+__host__ __device__ constexpr int kv4_row_bytes(int d) { return d / 2 + d / kKv4Group * 4; }
+
+cudaError_t launch_kv4_fill(const void* k, const void* v, int P, void* kc, void* vc, void* sk, void* sv, int B,
+                            int Hkv, int d, int W, int S, int sms, cudaStream_t stream);
+cudaError_t launch_kv4_append(const void* k, const void* v, const int32_t* pos, void* kc, void* vc, void* sk,
+                              void* sv, int B, int Hkv, int d, int W, int S, cudaStream_t stream);
+cudaError_t launch_kv4_read(const int32_t* positions, int n, const void* kc, const void* vc, const void* sk,
+                            const void* sv, void* k_out, void* v_out, bool f32, int B, int Hkv, int d, int W, int S,
+                            int sms, cudaStream_t stream);
+
+struct Kv4DecodeArgs {
+  const void* q;        // [B, Hq, d] bf16
+  const uint8_t* kc;    // [B, Hkv, W, row]
+  const uint8_t* vc;
+  const uint8_t* sk;    // [B, Hkv, S, row]
+  const uint8_t* sv;
+  const int32_t* pos;   // [B]
+  void* out;            // [B, Hq, d] bf16 or float32
+  float* lse;           // [B, Hq] or null
+  int B, Hq, Hkv, G, W, S;
+  float scale_log2;
+  int out_f32;
+};
+cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int d, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- eviction by weight
+struct HhDecodeArgs {
+  const void* q;            // [B, Hq, d] bf16
+  const void* kc;           // [B, Hkv, C, d] bf16
+  const void* vc;
+  const int32_t* slot_pos;  // [B, Hkv, C], < 0: empty
+  float* score;             // [B, Hkv, C], updated
+  void* out;                // [B, Hq, d] bf16 or float32
+  float* lse;               // [B, Hq] or null
+  int B, Hq, Hkv, G, C;
+  float scale_log2, decay;
+  int out_f32;
+};
+constexpr int kHhMaxCapacity = 16384;  // slots whose scores a cluster's shared memory holds (64 KB a block of 8)
+cudaError_t launch_hh_decode(const HhDecodeArgs& a, int d, int sms, cudaStream_t stream);
+cudaError_t launch_hh_append(const void* k, const void* v, const int32_t* pos, void* kc, void* vc,
+                             int32_t* slot_pos, float* score, int32_t* slot, int B, int Hkv, int d, int C, int S,
+                             int recent, cudaStream_t stream);
+cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, int L, void* kc, void* vc,
+                           int32_t* slot_pos, float* score, int B, int Hkv, int d, int C, int S, int recent, int sms,
+                           cudaStream_t stream);
+
+// ---------------------------------------------------------------- rotary positions with axes
+constexpr int kRopeMaxAxes = 4;
+struct RopeAxesTable {
+  double theta[64];       // per pair
+  unsigned char axis[64];
+};
+struct RopeAxesArgs {
+  void* q;
+  void* k;                  // may be null
+  const int32_t* positions; // [n_axes, T]
+  long long T, q_stride, k_stride;  // strides in elements between tokens
+  int Hq, Hkv, d;
+  float sign;               // +1 forward, -1 inverse
+};
+cudaError_t launch_rope_axes(const RopeAxesArgs& a, const RopeAxesTable& t, bool f32, int sms, cudaStream_t stream);
+
+}  // namespace swa

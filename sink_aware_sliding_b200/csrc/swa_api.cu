@@ -12,6 +12,8 @@
 
 #include "../../include/swa.h"
 #include "based_linear.h"
+#include "fixed_cache.h"
+#include "hh_scores.h"
 #include "swa_internal.h"
 
 namespace {
@@ -65,6 +67,7 @@ int device_info(DeviceInfo** out) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // 3-D tiled map over a [rows, heads, d] tensor: box = {128 bytes of d, 1 head, box_rows}.
 // atom32: 128-byte swizzle with 32-byte atoms (fp32 operands read in MN-major order).
@@ -536,6 +539,266 @@ int swa_based_linear_decode(const void* q, const void* k, const void* v, float* 
   if (static_cast<long long>(B) * H > INT32_MAX) return SWA_ERR_UNSUPPORTED;
   cudaError_t e = swa::launch_based_linear_decode(q, k, v, state, zsum, out, B, H, scale, out_dtype == SWA_DTYPE_F32,
                                                   reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+size_t swa_kv4_row_bytes(int d) { return d == 64 || d == 128 ? swa::kv4_row_bytes(d) : 0; }
+
+int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* vcache, void* sink_k, void* sink_v,
+                       int B, int Hkv, int d, int window, int n_sink, swa_stream_t stream) {
+  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  if (st != SWA_OK) return st;
+  if (P < 0) return SWA_ERR_INVALID_ARG;
+  if (P == 0 || B == 0) return SWA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return SWA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  cudaError_t e = swa::launch_kv4_fill(k, v, P, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink, dev->sms,
+                                       reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_kv4_cache_append(const void* k_new, const void* v_new, const int32_t* pos, void* kcache, void* vcache,
+                         void* sink_k, void* sink_v, int B, int Hkv, int d, int window, int n_sink,
+                         swa_stream_t stream) {
+  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  if (st != SWA_OK) return st;
+  if (B == 0) return SWA_OK;
+  if (static_cast<long long>(B) * Hkv > INT32_MAX) return SWA_ERR_UNSUPPORTED;
+  if (!k_new || !v_new || !pos || !aligned16(k_new) || !aligned16(v_new) || !aligned4(pos)) return SWA_ERR_INVALID_ARG;
+  cudaError_t e = swa::launch_kv4_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink,
+                                         reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_kv4_cache_read(const int32_t* positions, int n, const void* kcache, const void* vcache, const void* sink_k,
+                       const void* sink_v, void* k_out, void* v_out, int out_dtype, int B, int Hkv, int d, int window,
+                       int n_sink, swa_stream_t stream) {
+  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  if (st != SWA_OK) return st;
+  if (n < 0 || (out_dtype != SWA_DTYPE_BF16 && out_dtype != SWA_DTYPE_F32)) return SWA_ERR_INVALID_ARG;
+  if (n == 0 || B == 0) return SWA_OK;
+  if (!positions || !aligned4(positions) || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return SWA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  cudaError_t e = swa::launch_kv4_read(positions, n, kcache, vcache, sink_k, sink_v, k_out, v_out,
+                                       out_dtype == SWA_DTYPE_F32, B, Hkv, d, window, n_sink, dev->sms,
+                                       reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const void* sink_k, const void* sink_v,
+                   const int32_t* pos, void* out, float* lse, int B, int Hq, int Hkv, int d, int window, int n_sink,
+                   float scale, int out_dtype, swa_stream_t stream) {
+  int st = swa::decode_args_status(q, kcache, vcache, sink_k, sink_v, pos, out, lse, B, Hq, Hkv, d, window, n_sink,
+                                   scale, out_dtype);
+  if (st != SWA_OK) return st;
+  if (B == 0) return SWA_OK;
+  if (static_cast<long long>(B) * Hkv > INT32_MAX / 8 || static_cast<long long>(window) + n_sink > INT32_MAX / 2)
+    return SWA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  swa::Kv4DecodeArgs a{};
+  a.q = q;
+  a.kc = static_cast<const uint8_t*>(kcache);
+  a.vc = static_cast<const uint8_t*>(vcache);
+  a.sk = static_cast<const uint8_t*>(sink_k);
+  a.sv = static_cast<const uint8_t*>(sink_v);
+  a.pos = pos;
+  a.out = out;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.W = window;
+  a.S = n_sink;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out_f32 = out_dtype == SWA_DTYPE_BF16_F32OUT ? 1 : 0;
+  cudaError_t e = swa::launch_kv4_decode(a, d, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_hh_scores(const void* q, const void* k, const float* lse, float* score, int B, int Hq, int Hkv, int L, int d,
+                  int n_obs, int window, int n_sink, float scale, swa_stream_t stream) {
+  int st = check_heads(Hq, Hkv, d, window, n_sink, scale, SWA_DTYPE_BF16);
+  if (st != SWA_OK) return st;
+  if (B < 0 || L < 0 || n_obs < 0 || n_obs > L) return SWA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * L == 0) return SWA_OK;
+  if (!q || !k || !lse || !score || !aligned16(q) || !aligned16(k) || !aligned4(lse) || !aligned4(score))
+    return SWA_ERR_INVALID_ARG;
+  const long long T = static_cast<long long>(B) * L;
+  const long long units = static_cast<long long>(B) * Hkv * ((L + 127) / 128);
+  if (T > INT32_MAX - 128 || units > INT32_MAX || static_cast<long long>(n_obs) * (Hq / Hkv) > INT32_MAX / 2)
+    return SWA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  CUtensorMap tq, tk;
+  if ((st = make_map(&tq, q, false, d, Hq, T, 128)) != SWA_OK) return st;
+  if ((st = make_map(&tk, k, false, d, Hkv, T, 128)) != SWA_OK) return st;
+  swa::HhScoresArgs h{};
+  swa::PrefillArgs& a = h.pa;
+  a.n_seq = B;
+  a.L = L;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.window = std::min(window, L);
+  a.n_sink = n_sink;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.timeout_ns = g_timeout_ns.load();
+  a.debug_flags = g_debug_flags.load();
+  a.err = dev->err;
+  h.lse = lse;
+  h.score = score;
+  h.n_obs = n_obs;
+  h.n_units = static_cast<int>(units);
+  cudaError_t e = swa::launch_hh_scores(h, tq, tk, d, static_cast<int>(std::min<long long>(dev->sms, units)),
+                                        reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+static int check_hh(int B, int Hkv, int d, int capacity, int n_sink, int recent, const void* kc, const void* vc,
+                    const int32_t* slot_pos, const float* score) {
+  if (B < 0 || Hkv <= 0 || n_sink < 0 || recent < 1 || static_cast<long long>(n_sink) + recent > capacity)
+    return SWA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || capacity > swa::kHhMaxCapacity || static_cast<long long>(B) * Hkv > INT32_MAX / 1024)
+    return SWA_ERR_UNSUPPORTED;
+  if (B == 0) return SWA_OK;
+  if (!kc || !vc || !slot_pos || !score || !aligned16(kc) || !aligned16(vc) || !aligned4(slot_pos) || !aligned4(score))
+    return SWA_ERR_INVALID_ARG;
+  return SWA_OK;
+}
+
+int swa_hh_cache_fill(const void* k, const void* v, const float* score_in, int L, void* kcache, void* vcache,
+                      int32_t* slot_pos, float* score, int B, int Hkv, int d, int capacity, int n_sink, int recent,
+                      swa_stream_t stream) {
+  int st = check_hh(B, Hkv, d, capacity, n_sink, recent, kcache, vcache, slot_pos, score);
+  if (st != SWA_OK) return st;
+  if (L < 0) return SWA_ERR_INVALID_ARG;
+  if (B == 0) return SWA_OK;
+  if (L > 0 && (!k || !v || !score_in || !aligned16(k) || !aligned16(v) || !aligned4(score_in)))
+    return SWA_ERR_INVALID_ARG;
+  if (L > INT32_MAX - 4096) return SWA_ERR_UNSUPPORTED;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  cudaError_t e = swa::launch_hh_fill(k, v, score_in, L, kcache, vcache, slot_pos, score, B, Hkv, d, capacity, n_sink,
+                                      recent, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_hh_cache_append(const void* k_new, const void* v_new, const int32_t* pos, void* kcache, void* vcache,
+                        int32_t* slot_pos, float* score, int32_t* slot, int B, int Hkv, int d, int capacity,
+                        int n_sink, int recent, swa_stream_t stream) {
+  int st = check_hh(B, Hkv, d, capacity, n_sink, recent, kcache, vcache, slot_pos, score);
+  if (st != SWA_OK) return st;
+  if (B == 0) return SWA_OK;
+  if (!k_new || !v_new || !pos || !aligned16(k_new) || !aligned16(v_new) || !aligned4(pos) ||
+      (slot && !aligned4(slot)))
+    return SWA_ERR_INVALID_ARG;
+  cudaError_t e = swa::launch_hh_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot, B, Hkv, d, capacity,
+                                        n_sink, recent, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_hh_decode(const void* q, const void* kcache, const void* vcache, const int32_t* slot_pos, float* score,
+                  void* out, float* lse, int B, int Hq, int Hkv, int d, int capacity, float scale, float decay,
+                  int out_dtype, swa_stream_t stream) {
+  int st = check_hh(B, Hkv, d, capacity, 0, 1, kcache, vcache, slot_pos, score);
+  if (st != SWA_OK) return st;
+  if (Hq <= 0 || Hq % Hkv != 0 || !(scale > 0.f) || !std::isfinite(scale) || !(decay >= 0.f && decay <= 1.f) ||
+      (out_dtype != SWA_DTYPE_BF16 && out_dtype != SWA_DTYPE_BF16_F32OUT))
+    return SWA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 8) return SWA_ERR_UNSUPPORTED;
+  if (B == 0) return SWA_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || (lse && !aligned4(lse))) return SWA_ERR_INVALID_ARG;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != SWA_OK) return st;
+  swa::HhDecodeArgs a{};
+  a.q = q;
+  a.kc = kcache;
+  a.vc = vcache;
+  a.slot_pos = slot_pos;
+  a.score = score;
+  a.out = out;
+  a.lse = lse;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.C = capacity;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.decay = decay;
+  a.out_f32 = out_dtype == SWA_DTYPE_BF16_F32OUT ? 1 : 0;
+  cudaError_t e = swa::launch_hh_decode(a, d, dev->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
+}
+
+int swa_rope_axes_qk(void* q, void* k, const int32_t* positions, long long n_tokens, int Hq, int Hkv, int d,
+                     long long q_stride, long long k_stride, const int32_t* sections, int n_axes, int layout,
+                     double rope_base, int inverse, int dtype, swa_stream_t stream) {
+  if (k == nullptr) Hkv = 0;
+  if (n_tokens < 0 || Hq < 0 || Hkv < 0 || n_axes < 1 || !sections || !rope_base_ok(rope_base) ||
+      (dtype != SWA_DTYPE_BF16 && dtype != SWA_DTYPE_F32) || layout < SWA_ROPE_SECTIONS ||
+      layout > SWA_ROPE_INTERLEAVED)
+    return SWA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || n_axes > swa::kRopeMaxAxes || Hq > 65536 || Hkv > 65536) return SWA_ERR_UNSUPPORTED;
+  const int half = d / 2;
+  int sum = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (sections[a] < 0 || sections[a] > half) return SWA_ERR_INVALID_ARG;
+    sum += sections[a];
+    if (layout == SWA_ROPE_INTERLEAVED && a > 0 && sections[a] > 0 && a + n_axes * (sections[a] - 1) >= half)
+      return SWA_ERR_INVALID_ARG;
+  }
+  if (sum != half) return SWA_ERR_INVALID_ARG;
+  const long long unit = dtype == SWA_DTYPE_F32 ? 4 : 8;  // elements of 16 bytes
+  if ((Hq > 0 && (q_stride < static_cast<long long>(Hq) * d || q_stride % unit != 0)) ||
+      (Hkv > 0 && (k_stride < static_cast<long long>(Hkv) * d || k_stride % unit != 0)))
+    return SWA_ERR_INVALID_ARG;
+  if (n_tokens == 0 || Hq + Hkv == 0) return SWA_OK;
+  if (!positions || !aligned4(positions) || (Hq > 0 && (!q || !aligned16(q))) || (Hkv > 0 && !aligned16(k)))
+    return SWA_ERR_INVALID_ARG;
+  if (n_tokens > INT64_MAX / 64 / std::max(q_stride, k_stride)) return SWA_ERR_UNSUPPORTED;
+  swa::RopeAxesTable t;
+  int axis = 0, m = 0;  // sections and per-axis layouts: the current axis and pair within it
+  for (int i = 0; i < half; ++i) {
+    if (layout == SWA_ROPE_INTERLEAVED) {
+      const int a = i % n_axes;
+      axis = a > 0 && i / n_axes < sections[a] ? a : 0;
+    } else {
+      while (m == sections[axis]) {
+        ++axis;
+        m = 0;
+      }
+    }
+    t.axis[i] = static_cast<unsigned char>(axis);
+    t.theta[i] = layout == SWA_ROPE_PER_AXIS ? std::pow(rope_base, -static_cast<double>(m) / sections[axis])
+                                             : std::pow(rope_base, -2.0 * i / d);
+    ++m;
+  }
+  for (int i = half; i < 64; ++i) {
+    t.axis[i] = 0;
+    t.theta[i] = 0.0;
+  }
+  DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != SWA_OK) return st;
+  swa::RopeAxesArgs a{};
+  a.q = q;
+  a.k = k;
+  a.positions = positions;
+  a.T = n_tokens;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.sign = inverse ? -1.f : 1.f;
+  cudaError_t e = swa::launch_rope_axes(a, t, dtype == SWA_DTYPE_F32, dev->sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 

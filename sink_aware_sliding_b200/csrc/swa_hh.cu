@@ -1,0 +1,247 @@
+// Cache of fixed capacity that evicts by accumulated attention weight: filling it from
+// a prompt, and appending one token to it.
+//
+// Both choose by (class, score, index) with a total order on float32 scores: the bits
+// of a float, the sign flipped for positive and all bits for negative ones, order like
+// the values; -0 counts as 0 and a NaN as the lowest.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "fixed_cache.h"
+
+namespace swa {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ uint32_t order_bits(float s) {
+  if (s != s) return 0u;
+  const uint32_t u = __float_as_uint(s + 0.f);  // -0 + 0 = 0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// ---------------------------------------------------------------- append
+// One block per (b, KV head): the smallest of (class, score, slot) over the slots, where
+// class is 0 for the slot of this very position, 1 for an empty one, 2 for one that may
+// go and 3 for the others; then the row is written.
+constexpr int kAppendThreads = 256;
+__global__ void __launch_bounds__(kAppendThreads)
+    swa_hh_append_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, const int32_t* __restrict__ pos,
+                         uint4* kc, uint4* vc, int32_t* slot_pos, float* score, int32_t* slot, int Hkv, int vec,
+                         int C, int S, int recent) {
+  __shared__ unsigned long long s_best[kAppendThreads / 32];
+  const size_t seg = blockIdx.x;
+  const int p = pos[seg / Hkv];
+  if (p < 0) {
+    if (threadIdx.x == 0 && slot != nullptr) slot[seg] = -1;
+    return;
+  }
+  const int32_t* sp = slot_pos + seg * C;
+  const float* sc = score + seg * C;
+  unsigned long long best = ~0ull;
+  for (int i = threadIdx.x; i < C; i += kAppendThreads) {
+    const int at = sp[i];
+    const uint32_t bits = order_bits(sc[i]);
+    const bool may = at >= S && at <= p - recent;
+    const unsigned cls = at == p ? 0u : at < 0 ? 1u : may ? 2u : 3u;
+    // class in 2 bits, score in 32, slot in 30
+    const unsigned long long key = (static_cast<unsigned long long>(cls) << 62) |
+                                   (static_cast<unsigned long long>(cls < 2 ? 0u : bits) << 30) |
+                                   static_cast<unsigned>(i);
+    best = min(best, key);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(kFull, best, o));
+  if ((threadIdx.x & 31) == 0) s_best[threadIdx.x >> 5] = best;
+  __syncthreads();
+  best = s_best[0];
+#pragma unroll
+  for (int w = 1; w < kAppendThreads / 32; ++w) best = min(best, s_best[w]);
+  const int i = static_cast<int>(best & 0x3fffffffu);
+  const size_t row = (seg * C + i) * vec;
+  if (threadIdx.x < vec) kc[row + threadIdx.x] = k[seg * vec + threadIdx.x];
+  else if (threadIdx.x < 2 * vec) vc[row + threadIdx.x - vec] = v[seg * vec + threadIdx.x - vec];
+  if (threadIdx.x == 0) {
+    slot_pos[seg * C + i] = p;
+    score[seg * C + i] = 0.f;
+    if (slot != nullptr) slot[seg] = i;
+  }
+}
+
+// ---------------------------------------------------------------- fill
+// Select: one block per (b, KV head).  The `need` largest keys among the positions
+// S .. L - recent - 1 are found by a radix select on the ordered bits (11, 11 and 10
+// bits, histograms in shared memory): afterwards `cut` is the smallest kept key and
+// `ties` how many positions with exactly that key are kept, the earlier ones first.
+// Each warp then walks one contiguous stretch of positions, so that the kept ones come
+// out in ascending order after a prefix over the warps.
+constexpr int kFillThreads = 1024;
+constexpr int kFillWarps = kFillThreads / 32;
+__global__ void __launch_bounds__(kFillThreads)
+    swa_hh_select_kernel(const float* __restrict__ score_in, int L, int32_t* slot_pos, float* score, int C, int S,
+                         int recent) {
+  __shared__ unsigned s_hist[2048];
+  __shared__ unsigned s_cut, s_left;
+  __shared__ int s_kept[kFillWarps], s_ties[kFillWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float* in = score_in + static_cast<size_t>(blockIdx.x) * L;
+  int32_t* sp = slot_pos + static_cast<size_t>(blockIdx.x) * C;
+  float* sc = score + static_cast<size_t>(blockIdx.x) * C;
+  if (L <= C) {
+    for (int i = tid; i < C; i += kFillThreads) {
+      sp[i] = i < L ? i : -1;
+      sc[i] = i < L ? in[i] : 0.f;
+    }
+    return;
+  }
+  const int lo = S, hi = L - recent;          // positions that compete
+  unsigned prefix = 0, need = C - S - recent;  // need <= hi - lo, as L > C
+  // need = 0: nothing competes successfully; cut above every key
+  unsigned cut = 0xffffffffu, ties = 0;
+  if (need > 0) {
+    constexpr int kShift[3] = {21, 10, 0};
+    constexpr int kBits[3] = {11, 11, 10};
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = kShift[pass];
+      const unsigned bins = 1u << kBits[pass];
+      for (unsigned i = tid; i < bins; i += kFillThreads) s_hist[i] = 0;
+      __syncthreads();
+      for (int i = lo + tid; i < hi; i += kFillThreads) {
+        const uint32_t key = order_bits(in[i]);
+        if (pass == 0 || (key >> (shift + kBits[pass])) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // from the top: lane 0 has the largest bins
+        const unsigned per = bins / 32;
+        unsigned sum = 0;
+        for (unsigned i = 0; i < per; ++i) sum += s_hist[bins - 1 - (lane * per + i)];
+        unsigned incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned y = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += y;
+        }
+        unsigned above = incl - sum;
+        if (above < need && need <= incl) {  // one lane
+          for (unsigned i = 0; i < per; ++i) {
+            const unsigned bin = bins - 1 - (lane * per + i);
+            if (above + s_hist[bin] >= need) {
+              s_cut = (prefix << kBits[pass]) | bin;
+              s_left = need - above;
+              break;
+            }
+            above += s_hist[bin];
+          }
+        }
+      }
+      __syncthreads();
+      prefix = s_cut;
+      need = s_left;
+      __syncthreads();
+    }
+    cut = prefix;
+    ties = need;
+  }
+  // ---- compaction: stretch of this warp
+  const int per = ((L + kFillWarps - 1) / kFillWarps + 31) / 32 * 32;
+  const int first = min(L, warp * per), last = min(L, first + per);
+  int n_kept = 0, n_ties = 0;
+  for (int i0 = first; i0 < last; i0 += 32) {
+    const int i = i0 + lane;
+    bool above = false, equal = false;
+    if (i < last) {
+      const bool always = i < lo || i >= hi;
+      const uint32_t key = always ? 0u : order_bits(in[i]);
+      above = always || (ties > 0 && key > cut);
+      equal = !always && ties > 0 && key == cut;
+    }
+    n_kept += __popc(__ballot_sync(kFull, above));
+    n_ties += __popc(__ballot_sync(kFull, equal));
+  }
+  if (lane == 0) {
+    s_kept[warp] = n_kept;
+    s_ties[warp] = n_ties;
+  }
+  __syncthreads();
+  int out = 0, tie = 0;  // kept without ties, and ties, in the stretches before
+  for (int w = 0; w < warp; ++w) {
+    out += s_kept[w];
+    tie += s_ties[w];
+  }
+  for (int i0 = first; i0 < last; i0 += 32) {
+    const int i = i0 + lane;
+    bool above = false, equal = false;
+    float x = 0.f;
+    if (i < last) {
+      x = in[i];
+      const bool always = i < lo || i >= hi;
+      const uint32_t key = always ? 0u : order_bits(x);
+      above = always || (ties > 0 && key > cut);
+      equal = !always && ties > 0 && key == cut;
+    }
+    const unsigned ma = __ballot_sync(kFull, above), me = __ballot_sync(kFull, equal);
+    const unsigned below = (1u << lane) - 1;
+    const int my_tie = tie + __popc(me & below);
+    const int slot = out + __popc(ma & below) + min(my_tie, static_cast<int>(ties));
+    if (above || (equal && my_tie < static_cast<int>(ties))) {
+      sp[slot] = i;
+      sc[slot] = x;
+    }
+    out += __popc(ma);
+    tie += __popc(me);
+  }
+}
+
+// Copy the chosen rows, one thread per 16 bytes, `per` blocks a (b, KV head).
+__global__ void __launch_bounds__(256)
+    swa_hh_gather_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, int L, uint4* __restrict__ kc,
+                         uint4* __restrict__ vc, const int32_t* __restrict__ slot_pos, int Hkv, int vec, int C,
+                         int kept, int per) {
+  const size_t seg = blockIdx.x / per;
+  const size_t b = seg / Hkv, h = seg % Hkv;
+  const int total = kept * vec;
+  for (int i = blockIdx.x % per * 256 + threadIdx.x; i < total; i += per * 256) {
+    const int s = i / vec, e = i % vec;
+    const int p = slot_pos[seg * C + s];
+    const size_t src = ((b * L + p) * Hkv + h) * vec + e;
+    const size_t dst = (seg * C + s) * vec + e;
+    kc[dst] = k[src];
+    vc[dst] = v[src];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_hh_append(const void* k, const void* v, const int32_t* pos, void* kc, void* vc,
+                             int32_t* slot_pos, float* score, int32_t* slot, int B, int Hkv, int d, int C, int S,
+                             int recent, cudaStream_t stream) {
+  swa_hh_append_kernel<<<B * Hkv, kAppendThreads, 0, stream>>>(
+      static_cast<const uint4*>(k), static_cast<const uint4*>(v), pos, static_cast<uint4*>(kc),
+      static_cast<uint4*>(vc), slot_pos, score, slot, Hkv, d / 8, C, S, recent);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, int L, void* kc, void* vc,
+                           int32_t* slot_pos, float* score, int B, int Hkv, int d, int C, int S, int recent, int sms,
+                           cudaStream_t stream) {
+  const int segs = B * Hkv;
+  swa_hh_select_kernel<<<segs, kFillThreads, 0, stream>>>(score_in, L, slot_pos, score, C, S, recent);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int kept = std::min(L, C);
+  if (kept == 0) return cudaSuccess;
+  const int vec = d / 8;
+  const int blocks = (kept * vec + 255) / 256;
+  const int x = std::min(blocks, std::max(1, (sms * 32 + segs - 1) / segs));
+  swa_hh_gather_kernel<<<static_cast<unsigned>(x) * segs, 256, 0, stream>>>(
+      static_cast<const uint4*>(k), static_cast<const uint4*>(v), L, static_cast<uint4*>(kc), static_cast<uint4*>(vc),
+      slot_pos, Hkv, vec, C, kept, x);
+  return cudaGetLastError();
+}
+
+}  // namespace swa

@@ -1,0 +1,287 @@
+// Attention weight that the keys of a prompt received from its last queries:
+//     score[j] = sum over observing queries t and query heads g of exp(scale q_tg . k_j - lse_tg).
+//
+// Only column sums are wanted and the rows' log-sum-exps are known, so there is no
+// running softmax and no second product: a work unit is one tile of 128 keys of one
+// (sequence, KV head), its K tile is loaded once, and the tiles of 128 observing queries
+// of each head stream past it.  S^T = K Q^T runs on tcgen05 with the keys as the 128
+// TMEM lanes: a thread owns one key and adds up its row of exponentials, without any
+// exchange between threads.  Four S tiles in TMEM and two warpgroups that take every
+// other tile keep the exponentials, which bound the kernel (16 a cycle and SM against
+// 4096 multiply-adds: at d = 128 twice the product's time), from waiting for products.
+// Sums: float32 over a tile's 128 columns in four chains, float64 over the tiles.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "hh_scores.h"
+#include "prefill_common.cuh"
+#include "ptx.cuh"
+
+namespace swa {
+namespace {
+
+using prefill::Ctl;
+using prefill::wait_bar;
+
+constexpr int kThreads = 320;  // two warpgroups of exponentials, a load warp, an MMA warp
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kBuf = 4;        // S tiles in TMEM
+constexpr int kQStages = 3;
+
+template <int D>
+struct Cfg {
+  static constexpr int TILE = 128 * D * 2;                // bytes of a K or Q tile
+  static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a tile
+  static constexpr int OFF_K = 0;                         // two K tiles
+  static constexpr int OFF_Q = 2 * TILE;
+  static constexpr int OFF_LSE = OFF_Q + kQStages * TILE;  // [8 warps][128] floats
+  static constexpr int OFF_SUM = OFF_LSE + 8 * 128 * 4;    // [128] doubles
+  static constexpr int OFF_BAR = OFF_SUM + 128 * 8;
+  static constexpr int NBAR = 4 + 2 * kQStages + 2 * kBuf + 3;
+  static constexpr int SMEM = OFF_BAR + 8 * NBAR + 16 + 1024;
+};
+
+// One tile of keys of (b, kvh) and the observing queries that see any of them.
+struct Unit {
+  int b, kvh, j0, qt_lo, n_qt;
+};
+
+__device__ __forceinline__ Unit get_unit(const HhScoresArgs& a, int u) {
+  Unit x;
+  const int segs = a.pa.n_seq * a.pa.Hkv;
+  const int seg = u % segs;
+  x.b = seg / a.pa.Hkv;
+  x.kvh = seg % a.pa.Hkv;
+  x.j0 = u / segs * 128;
+  const int L = a.pa.L, t_first = L - a.n_obs;
+  const int j1 = min(x.j0 + 127, L - 1);
+  const int lo = max(t_first, x.j0);                                    // first query that sees a key here
+  const int hi = x.j0 < a.pa.n_sink ? L - 1 : min(L - 1, j1 + a.pa.window - 1);  // last one; window <= L
+  x.qt_lo = (lo - t_first) / 128;
+  x.n_qt = hi < lo ? 0 : (hi - t_first) / 128 - x.qt_lo + 1;
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    swa_hh_scores_kernel(const __grid_constant__ HhScoresArgs a, const __grid_constant__ CUtensorMap tq,
+                         const __grid_constant__ CUtensorMap tk) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  uint32_t bar = base + C::OFF_BAR;
+  const uint32_t k_full = bar, k_empty = bar + 16, q_full = bar + 32, q_empty = q_full + 8 * kQStages,
+                 s_full = q_empty + 8 * kQStages, s_empty = s_full + 8 * kBuf, sum_full = s_empty + 8 * kBuf, sum_empty = sum_full + 8, drain = sum_full + 16;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(gbase + C::OFF_BAR + 8 * C::NBAR);
+  Ctl ctl{reinterpret_cast<volatile int*>(gbase + C::OFF_BAR + 8 * C::NBAR + 4), &a.pa};
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kQStages; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kBuf; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, 128);
+    }
+    mbar_init(sum_full, 128);
+    mbar_init(sum_empty, 128);
+    mbar_init(drain, 1);
+    *ctl.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base;
+  const int G = a.pa.G, L = a.pa.L;
+  const int t_first = L - a.n_obs;
+
+  if (warp == kLoadWarp) {
+    if (lane == 0) {
+      int uc = 0, n = 0;  // units with work, Q tiles
+      bool ok = (a.pa.debug_flags & 1) == 0;
+      for (int u = blockIdx.x; ok && u < a.n_units; u += gridDim.x) {
+        const Unit x = get_unit(a, u);
+        if (x.n_qt == 0) continue;
+        const int kb = uc & 1;
+        if (!(ok = wait_bar(k_empty + 8 * kb, ((uc >> 1) & 1) ^ 1, ctl))) break;
+        mbar_expect_tx(k_full + 8 * kb, C::TILE);
+        for (int c = 0; c < C::NCHUNK; ++c)
+          tma_load_3d(base + C::OFF_K + kb * C::TILE + c * (128 * 128), &tk, k_full + 8 * kb, c * 64, x.kvh,
+                      x.b * L + x.j0);
+        ++uc;
+        for (int h = 0; ok && h < G; ++h)
+          for (int i = 0; i < x.n_qt; ++i, ++n) {
+            const int st = n % kQStages;
+            if (!(ok = wait_bar(q_empty + 8 * st, ((n / kQStages) & 1) ^ 1, ctl))) break;
+            mbar_expect_tx(q_full + 8 * st, C::TILE);
+            for (int c = 0; c < C::NCHUNK; ++c)
+              tma_load_3d(base + C::OFF_Q + st * C::TILE + c * (128 * 128), &tq, q_full + 8 * st, c * 64,
+                          x.kvh * G + h, x.b * L + t_first + (x.qt_lo + i) * 128);
+          }
+      }
+      if (*ctl.abort_flag) {  // copies in flight land before the block ends
+        for (int i = max(0, uc - 2); i < uc; ++i) wait_bar(k_full + 8 * (i & 1), (i >> 1) & 1, ctl, false);
+        for (int i = max(0, n - kQStages); i < n; ++i)
+          wait_bar(q_full + 8 * (i % kQStages), (i / kQStages) & 1, ctl, false);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      constexpr uint32_t kIdesc = make_idesc(1u, 128, 128, false);
+      int uc = 0, n = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < a.n_units; u += gridDim.x) {
+        const Unit x = get_unit(a, u);
+        if (x.n_qt == 0) continue;
+        const int kb = uc & 1;
+        if (!(ok = wait_bar(k_full + 8 * kb, (uc >> 1) & 1, ctl))) break;
+        const uint32_t ks = base + C::OFF_K + kb * C::TILE;
+        const int count = x.n_qt * G;
+        for (int i = 0; i < count; ++i, ++n) {
+          const int st = n % kQStages, sb = n & (kBuf - 1);
+          if (!(ok = wait_bar(s_empty + 8 * sb, ((n / kBuf) & 1) ^ 1, ctl))) break;
+          if (!(ok = wait_bar(q_full + 8 * st, (n / kQStages) & 1, ctl))) break;
+          tc_fence_after();
+          const uint32_t qs = base + C::OFF_Q + st * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+            umma_ss<false>(tmem + 128 * sb, smem_desc(ks + off, 16, 1024, kLayoutSw128),
+                           smem_desc(qs + off, 16, 1024, kLayoutSw128), kIdesc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(s_full + 8 * sb);
+          tc_commit(q_empty + 8 * st);
+        }
+        if (ok) tc_commit(k_empty + 8 * kb);
+        ++uc;
+      }
+      if (*ctl.abort_flag) {  // every product issued is done before TMEM is freed
+        tc_commit(drain);
+        wait_bar(drain, 0, ctl, false);
+      }
+    }
+    __syncwarp();
+  } else {
+    const int wg = warp >> 2, row = tid & 127;
+    float* lse = reinterpret_cast<float*>(gbase + C::OFF_LSE) + warp * 128;
+    double* s_sum = reinterpret_cast<double*>(gbase + C::OFF_SUM);
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint64_t sl2 = f2_pack(a.pa.scale_log2, a.pa.scale_log2);
+    int n = 0, uc = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < a.n_units; u += gridDim.x, ++uc) {
+      const Unit x = get_unit(a, u);
+      const int j = x.j0 + row;
+      // queries that see key j: [j, last]
+      const int last = j >= L ? -1 : j < a.pa.n_sink ? L - 1 : min(L - 1, j + a.pa.window - 1);
+      const int count = x.n_qt * G;
+      double total = 0.0;
+      for (int i = 0; i < count; ++i, ++n) {
+        if ((n & 1) != wg) continue;
+        const int h = i / x.n_qt, qt = x.qt_lo + i - h * x.n_qt;
+        const int t0 = t_first + qt * 128;
+        {  // each warp keeps its own copy of the tile's -lse log2(e): no barrier between warps
+          const float* src = a.lse + (static_cast<size_t>(x.b) * a.pa.Hq + x.kvh * G + h) * L + t0;
+          __syncwarp();
+#pragma unroll
+          for (int c = lane; c < 128; c += 32) lse[c] = t0 + c < L ? src[c] * -1.4426950408889634f : 0.f;
+          __syncwarp();
+        }
+        const int sb = n & (kBuf - 1);
+        ok = __all_sync(0xffffffffu, wait_bar(s_full + 8 * sb, (n / kBuf) & 1, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        // every key here sees every query of the tile?
+        const bool whole = x.j0 + 127 <= t0 && t0 + 127 < L &&
+                           (t0 + 127 <= x.j0 + a.pa.window - 1 || x.j0 + 127 < a.pa.n_sink);
+        const int c_lo = j - t0, c_hi = last - t0;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          uint32_t r[32];
+          tmem_ld32_wait(tmem + 128 * sb + lane_off + c0, r);
+          if (c0 == 96) {
+            tc_fence_before();
+            mbar_arrive(s_empty + 8 * sb);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(lse + c0 + c);
+            float e[4];
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2, f2_pack(w.x, w.y)), e[0],
+                      e[1]);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2, f2_pack(w.z, w.w)),
+                      e[2], e[3]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float p = ex2_approx(e[q]);
+              if (!whole) p = (c0 + c + q >= c_lo && c0 + c + q <= c_hi) ? p : 0.f;
+              part[q] += p;
+            }
+          }
+        }
+        total += static_cast<double>((part[0] + part[1]) + (part[2] + part[3]));
+      }
+      if (!ok) break;
+      // the two warpgroups' sums; bounded waits, so that an abort ends them too
+      if (wg == 1) {
+        ok = __all_sync(0xffffffffu, wait_bar(sum_empty, (uc & 1) ^ 1, ctl));
+        if (!ok) break;
+        s_sum[row] = total;
+        mbar_arrive(sum_full);
+      } else {
+        ok = __all_sync(0xffffffffu, wait_bar(sum_full, uc & 1, ctl));
+        if (!ok) break;
+        total += s_sum[row];
+        mbar_arrive(sum_empty);
+        if (j < L) a.score[(static_cast<size_t>(x.b) * a.pa.Hkv + x.kvh) * L + j] = static_cast<float>(total);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_impl(const HhScoresArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, int grid,
+                        cudaStream_t stream) {
+  auto kern = swa_hh_scores_kernel<D>;
+  static_assert(Cfg<D>::SMEM <= 232448, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, Cfg<D>::SMEM, stream>>>(a, tq, tk);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_hh_scores(const HhScoresArgs& a, const CUtensorMap& tq, const CUtensorMap& tk, int d, int grid,
+                             cudaStream_t stream) {
+  return d == 128 ? launch_impl<128>(a, tq, tk, grid, stream) : launch_impl<64>(a, tq, tk, grid, stream);
+}
+
+}  // namespace swa

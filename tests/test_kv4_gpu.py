@@ -1,0 +1,271 @@
+"""4-bit ring cache on the GPU (through the C ABI) against the fp64 oracle: packed rows bit for bit, values
+read back, the decode step, and a run of prompt, appends and decodes.
+
+Tolerances of the decode.  The kernel rounds p * step to fp16 (relative 2^-11 of the value with truncation and
+the fp16 product's rounding together; finfo(float16).eps / 2 = 2^-11), and a code is at most 15, so that an output
+moves by at most 2^-11 * max(15 step).  A score is a float32 sum of d products of magnitude sum |q||k| scale: at most
+(d + 16) 2^-24 of that (and 2^-20 to allow for the matrix unit's own alignment), and an output moves by twice the
+score's error times max |v|, a log-sum-exp by once.  A bf16 output is rounded by at most half a step, 2^-8."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sink_aware_sliding_b200 as swa
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).bfloat16()
+
+
+class Cache:
+    def __init__(self, B, H, d, W, S, fill=0):
+        row = swa.swa_kv4_row_bytes(d)
+        self.kc, self.vc = (torch.full((B, H, W, row), fill, dtype=torch.uint8, device="cuda") for _ in range(2))
+        self.sk, self.sv = (torch.full((B, H, S, row), fill, dtype=torch.uint8, device="cuda") for _ in range(2))
+        self.W, self.S = W, S
+
+    def args(self):
+        return self.kc, self.vc, self.sk, self.sv
+
+
+def bounds(q, k, v, scale, seen):
+    """Largest allowed error of an output (before its rounding) and of a log-sum-exp; k, v [n, d] values."""
+    k, v = k[seen], v[seen]
+    size = scale * (np.abs(q) @ np.abs(k).T).max()
+    dz = size * ((q.shape[-1] + 16) * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -21
+    span = max(float(oracle.kv4_quantise(v)[1].max()) * 15, 0.0)
+    return 2.0 ** -11 * span + 2 * dz * np.abs(v).max() + 1e-30, dz + 4e-7 * 40
+
+
+def check_decode(c, q, pos, kval, vval, scale=None, f32=True):
+    """Decode and compare; kval, vval [B, H, W + S, d] are the values in the slots."""
+    B, Hq, d = q.shape
+    H = kval.shape[1]
+    out = torch.full((B, Hq, d), 7.0, device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)
+    lse = torch.full((B, Hq), 7.0, device="cuda")
+    swa.swa_kv4_decode(q.cuda(), *c.args(), torch.tensor(pos, dtype=torch.int32, device="cuda"), out, lse, c.W, c.S,
+                       scale)
+    torch.cuda.synchronize()
+    scale = scale or 1 / math.sqrt(d)
+    got, gl, q64 = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    for b in range(B):
+        p = int(pos[b])
+        i = np.arange(c.W + c.S)
+        seen = np.where(i < c.W, i < min(p + 1, c.W), i - c.W < min(c.S, max(0, p - c.W + 1)))
+        for h in range(Hq):
+            kv = h // (Hq // H)
+            if not seen.any():
+                assert (got[b, h] == 0).all() and gl[b, h] == -np.inf
+                continue
+            z = scale * kval[b, kv][seen] @ q64[b, h]
+            e = np.exp(z - z.max())
+            want, wl = e @ vval[b, kv][seen] / e.sum(), z.max() + np.log(e.sum())
+            tol, tl = bounds(q64[b, h], kval[b, kv], vval[b, kv], scale, seen)
+            tol = tol + (0 if f32 else 2.0 ** -8 * np.abs(want))
+            assert (np.abs(got[b, h] - want) <= tol).all(), (b, h, np.abs(got[b, h] - want).max(), tol)
+            assert abs(gl[b, h] - wl) <= tl, (b, h, gl[b, h], wl)
+
+
+def slots(kval, B, H, W, S, d, seed, scale=1.0):
+    return rand((B, H, W, d), seed, scale), rand((B, H, S, d), seed + 1, scale)
+
+
+def filled(B, H, d, W, S, seed, scale=1.0):
+    """A cache whose every slot holds something, and the values."""
+    c = Cache(B, H, d, W, S)
+    vals = []
+    for ring, sink, s in ((c.kc, c.sk, seed), (c.vc, c.sv, seed + 10)):
+        r, k = rand((B, H, W, d), s, scale), rand((B, H, S, d), s + 1, scale)
+        ring.copy_(torch.from_numpy(oracle.kv4_pack(r)))
+        if S:
+            sink.copy_(torch.from_numpy(oracle.kv4_pack(k)))
+        vals.append(np.concatenate([oracle.kv4_values(r), oracle.kv4_values(k)], 2))
+    return c, vals[0], vals[1]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("P,W,S", [(1, 1, 0), (5, 8, 3), (8, 8, 8), (9, 8, 4), (200, 64, 4), (70, 64, 70), (33, 7, 0)])
+def test_fill_is_bit_exact(d, P, W, S):
+    B, H = 2, 3
+    k, v = rand((B, P, H, d), P + d), rand((B, P, H, d), P + d + 1)
+    c = Cache(B, H, d, W, S, fill=171)
+    swa.swa_kv4_cache_fill(k.cuda(), v.cuda(), *c.args(), W, S)
+    torch.cuda.synchronize()
+    for x, ring, sink in ((k, c.kc, c.sk), (v, c.vc, c.sv)):
+        rows = oracle.kv4_pack(x)
+        want_ring = np.full((B, H, W, rows.shape[-1]), 171, dtype=np.uint8)
+        want_sink = np.full((B, H, S, rows.shape[-1]), 171, dtype=np.uint8)
+        for p in range(max(0, P - W), P):
+            want_ring[:, :, p % W] = rows[:, p]
+        for p in range(min(P, S)):
+            want_sink[:, :, p] = rows[:, p]
+        np.testing.assert_array_equal(ring.cpu().numpy(), want_ring)
+        np.testing.assert_array_equal(sink.cpu().numpy(), want_sink)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_of_every_kind_are_quantised_as_defined(d):
+    """Constant groups, zeros, tiny and large values, one outlier, and values that lie on a rounding border."""
+    B, H, P = 1, 1, 64
+    x = rand((B, P, H, d), 5).float()
+    x[0, 0] = 0
+    x[0, 1] = 2.5
+    x[0, 2] = -3
+    x[0, 3] *= 1e-30
+    x[0, 4] *= 1e30
+    x[0, 5] *= 1e-38  # steps below 2^-126
+    x[0, 6, 0, 7] = 1000
+    x[0, 7, 0, :] = torch.arange(d) % 32  # 31 / 15 steps
+    x[0, 8, 0, :] = (torch.arange(d) % 31).float() / 2  # step 1: halves are borders
+    x[0, 9, 0, ::2] = -0.0
+    k = x.bfloat16()
+    c = Cache(B, H, d, P, 0)
+    swa.swa_kv4_cache_fill(k.cuda(), (-k).cuda(), *c.args(), P, 0)
+    out = [torch.empty(B, P, H, d, device="cuda") for _ in range(2)]
+    swa.swa_kv4_cache_read(torch.arange(P, dtype=torch.int32, device="cuda")[None], *c.args(), *out, P, 0)
+    torch.cuda.synchronize()
+    for got, src in zip(out, (k, -k)):
+        # one float32 rounding of code * step + lo
+        np.testing.assert_array_equal(got.cpu().numpy(), oracle.kv4_values(src).astype(np.float32))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_and_read_back(d):
+    B, H, W, S = 4, 2, 6, 3
+    c = Cache(B, H, d, W, S)
+    held = {}
+    for step in range(20):
+        pos = [step, step + 5, -1 if step % 3 == 0 else step, 2 ** 31 - 30 + step]
+        k, v = rand((B, H, d), step), rand((B, H, d), 100 + step)
+        swa.swa_kv4_cache_append(k.cuda(), v.cuda(), torch.tensor(pos, dtype=torch.int32, device="cuda"), *c.args(),
+                                 W, S)
+        for b, p in enumerate(pos):
+            if p >= 0:
+                held[b, p] = (oracle.kv4_values(k[b]), oracle.kv4_values(v[b]))
+    ask = torch.full((B, 8), -1, dtype=torch.int32)
+    ask[0, :6] = torch.arange(14, 20)
+    ask[0, 6:] = torch.tensor([0, 2])
+    ask[1, 0] = 24
+    ask[2, 0] = 19
+    ask[3, 1] = 2 ** 31 - 11
+    for dt in (torch.float32, torch.bfloat16):
+        ko, vo = (torch.full((B, 8, H, d), 9.0, device="cuda", dtype=dt) for _ in range(2))
+        swa.swa_kv4_cache_read(ask.cuda(), *c.args(), ko, vo, W, S)
+        torch.cuda.synchronize()
+        for b in range(B):
+            for i in range(8):
+                p = int(ask[b, i])
+                want = held[b, p] if p >= 0 else (np.zeros((H, d)),) * 2
+                for got, w in zip((ko, vo), want):
+                    w = torch.from_numpy(w).float().to(dt)
+                    assert torch.equal(got[b, i].cpu(), w), (b, i)
+
+
+@pytest.mark.parametrize("d,Hq,H", [(64, 2, 2), (64, 8, 1), (128, 8, 2), (128, 7, 1), (128, 3, 3), (64, 12, 4)])
+@pytest.mark.parametrize("W,S", [(1, 0), (15, 1), (16, 16), (130, 4), (700, 20)])
+def test_decode_matches_oracle(d, Hq, H, W, S):
+    B = 5
+    c, kv, vv = filled(B, H, d, W, S, W + d)
+    pos = [W + S + 3, 0, W - 1, W, -1]
+    check_decode(c, rand((B, Hq, d), 3), pos, kv, vv)
+    check_decode(c, rand((B, Hq, d), 4), pos, kv, vv, f32=False)
+
+
+@pytest.mark.parametrize("B,W", [(1, 4096), (3, 20000), (40, 257)])
+def test_decode_long_and_wide(B, W):
+    """Every size of cluster."""
+    c, kv, vv = filled(B, 2, 128, W, 4, 11)
+    check_decode(c, rand((B, 8, 128), 12), [2 * W] * (B - 1) + [W // 2], kv, vv)
+
+
+@pytest.mark.parametrize("qs,ks,vs", [(1e-12, 1, 1), (1, 1e-20, 1e-20), (1e4, 1e-4, 1e6), (8, 8, 1e15), (0, 1, 1)])
+def test_decode_over_the_range_of_values(qs, ks, vs):
+    """Magnitudes far from 1, large scores (one key takes all), zero queries, and steps that differ by 2^40 within
+    one cache: the keys' order is turned so that the largest come first for one head and last for the other."""
+    B, H, d, W = 2, 2, 128, 200
+    c, kv, vv = filled(B, H, d, W, 0, 21)
+    k = rand((B, H, W, d), 22, ks)
+    v = rand((B, H, W, d), 23, vs).float()
+    v[:, 0, 50:] *= 2.0 ** -20
+    v[:, 1, :150] *= 2.0 ** -20
+    v = v.bfloat16()
+    c.kc.copy_(torch.from_numpy(oracle.kv4_pack(k)))
+    c.vc.copy_(torch.from_numpy(oracle.kv4_pack(v)))
+    check_decode(c, rand((B, 4, d), 24, qs), [W, W // 3], oracle.kv4_values(k), oracle.kv4_values(v))
+
+
+def test_slots_that_are_not_visible_are_not_read_into_the_result():
+    """A ring that is not full: what lies behind the last position holds NaN parameters."""
+    B, H, d, W, S = 1, 1, 128, 64, 4
+    c, kv, vv = filled(B, H, d, W, S, 31)
+    for t in (c.kc, c.vc):
+        t[:, :, 20:] = 255  # bf16 0xffff is a NaN
+    for t in (c.sk, c.sv):
+        t[:] = 255
+    check_decode(c, rand((B, 4, d), 32), [19], kv, vv)
+
+
+def test_a_prompt_and_generated_tokens_in_turn():
+    """Fill, then append and decode step by step, against attention over the quantised history."""
+    B, P, steps, H, Hq, d, W, S = 2, 90, 30, 2, 4, 64, 50, 3
+    c = Cache(B, H, d, W, S)
+    hist = [rand((B, P + steps, H, d), s) for s in (41, 42)]
+    swa.swa_kv4_cache_fill(hist[0][:, :P].contiguous().cuda(), hist[1][:, :P].contiguous().cuda(), *c.args(), W, S)
+    vals = [oracle.kv4_values(x) for x in hist]
+    for p in range(P, P + steps):
+        pos = torch.full((B,), p, dtype=torch.int32, device="cuda")
+        swa.swa_kv4_cache_append(hist[0][:, p].contiguous().cuda(), hist[1][:, p].contiguous().cuda(), pos, *c.args(),
+                                 W, S)
+        q = rand((B, Hq, d), p)
+        out, lse = torch.empty(B, Hq, d, device="cuda"), torch.empty(B, Hq, device="cuda")
+        swa.swa_kv4_decode(q.cuda(), *c.args(), pos, out, lse, W, S)
+        seen = oracle.visible_mask(p + 1, W, S)[p]
+        for b in range(B):
+            for h in range(Hq):
+                k, v = vals[0][b, :p + 1, h // 2], vals[1][b, :p + 1, h // 2]
+                z = k[seen] @ q[b, h].double().numpy() / math.sqrt(d)
+                e = np.exp(z - z.max())
+                tol, tl = bounds(q[b, h].double().numpy(), k, v, 1 / math.sqrt(d), seen)
+                assert np.abs(out[b, h].double().cpu().numpy() - e @ v[seen] / e.sum()).max() <= tol
+                assert abs(float(lse[b, h]) - z.max() - np.log(e.sum())) <= tl
+
+
+def test_captured_and_on_two_streams():
+    """A captured step replayed with new inputs, while another stream decodes from another cache; results as alone."""
+    B, H, Hq, d, W, S = 3, 2, 8, 128, 300, 4
+    ca, _, _ = filled(B, H, d, W, S, 51)
+    cb, _, _ = filled(B, H, d, W, S, 61)
+    q = rand((B, Hq, d), 52).cuda()
+    pos = torch.tensor([400, 20, 299], dtype=torch.int32, device="cuda")
+    kn, vn = rand((B, H, d), 53).cuda(), rand((B, H, d), 54).cuda()
+
+    def step(c, out, lse):
+        swa.swa_kv4_cache_append(kn, vn, pos, *c.args(), W, S)
+        swa.swa_kv4_decode(q, *c.args(), pos, out, lse, W, S)
+
+    alone = []
+    for c in (ca, cb):
+        out, lse = torch.empty(B, Hq, d, device="cuda", dtype=torch.bfloat16), torch.empty(B, Hq, device="cuda")
+        step(c, out, lse)
+        alone.append((out, lse))
+    torch.cuda.synchronize()
+    out, lse = torch.zeros_like(alone[0][0]), torch.zeros_like(alone[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(ca, out, lse)
+    side = torch.cuda.Stream()
+    ob, lb = torch.zeros_like(out), torch.zeros_like(lse)
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        graph.replay()
+        with torch.cuda.stream(side):
+            step(cb, ob, lb)
+    torch.cuda.synchronize()
+    assert torch.equal(out, alone[0][0]) and torch.equal(lse, alone[0][1])
+    assert torch.equal(ob, alone[1][0]) and torch.equal(lb, alone[1][1])
