@@ -390,23 +390,41 @@ def swa_kv4_row_bytes(d: int) -> int:
     return int(_load().swa_kv4_row_bytes(int(d)))
 
 
-def _gpu(t, name: str, dtype, shape) -> int:
-    """The address of a contiguous CUDA tensor on the current device, of this type and shape."""
-    import torch
-    _need(t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous(),
-          f"{name}: contiguous CUDA tensor, {dtype}, {list(shape)}")
-    _need(t.get_device() == torch.cuda.current_device(), f"{name}: on the current device")
-    return t.data_ptr()
+class _Args:
+    """Addresses of one call's tensors, each checked: contiguous, on the current device, of the type and shape
+    named.  The checks read as little as they can and put no text together unless they fail: a decode step's
+    launches take a few microseconds, and so should what comes before them."""
+
+    __slots__ = ("dev",)
+
+    def __init__(self, t, name: str):
+        import torch
+        if not t.is_cuda:
+            raise ValueError(f"{name}: CUDA tensor")
+        self.dev = torch.cuda.current_device()
+
+    def __call__(self, t, name: str, dtype, shape) -> int:
+        if t.dtype is not dtype or t.get_device() != self.dev or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on the current CUDA device")
+        return t.data_ptr()
+
+    def stream(self, stream):
+        if stream is not None:
+            return _stream(stream)
+        import torch
+        return torch._C._cuda_getCurrentRawStream(self.dev)
 
 
-def _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
+def _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
     import torch
+    u8 = torch.uint8
     row = d // 2 + d // 8
-    ring, sink = (B, Hkv, window, row), (B, Hkv, n_sink, row)
-    addr = [_gpu(kcache, "kcache", torch.uint8, ring), _gpu(vcache, "vcache", torch.uint8, ring), None, None]
-    if n_sink > 0:
-        addr[2:] = _gpu(sink_k, "sink_k", torch.uint8, sink), _gpu(sink_v, "sink_v", torch.uint8, sink)
-    return addr
+    ring = (B, Hkv, window, row)
+    if n_sink <= 0:
+        return at(kcache, "kcache", u8, ring), at(vcache, "vcache", u8, ring), None, None
+    sink = (B, Hkv, n_sink, row)
+    return (at(kcache, "kcache", u8, ring), at(vcache, "vcache", u8, ring), at(sink_k, "sink_k", u8, sink),
+            at(sink_v, "sink_v", u8, sink))
 
 
 def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink: int, stream=None) -> None:
@@ -414,11 +432,13 @@ def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink
     kcache/vcache [B, Hkv, window, row] uint8, sink_k/sink_v [B, Hkv, n_sink, row] (None without sinks)."""
     import torch
     _need(k.dim() == 4, "k [B, P, Hkv, d]")
-    B, P, Hkv, d = k.shape
-    kp, vp = _gpu(k, "k", torch.bfloat16, k.shape), _gpu(v, "v", torch.bfloat16, k.shape)
-    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, _stream(stream))
-    _check(st, "swa_kv4_cache_fill")
+    at = _Args(k, "k")
+    B, P, Hkv, d = shape = k.shape
+    kp, vp = at(k, "k", torch.bfloat16, shape), at(v, "v", torch.bfloat16, shape)
+    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, at.stream(stream))
+    if st:
+        _check(st, "swa_kv4_cache_fill")
 
 
 def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, window: int, n_sink: int,
@@ -426,12 +446,14 @@ def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, wind
     """Quantise k_new/v_new [B, Hkv, d] (bf16) of positions pos (int32 [B]) into the 4-bit ring cache."""
     import torch
     _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
-    B, Hkv, d = k_new.shape
-    kp, vp = _gpu(k_new, "k_new", torch.bfloat16, k_new.shape), _gpu(v_new, "v_new", torch.bfloat16, k_new.shape)
-    pp = _gpu(pos, "pos", torch.int32, (B,))
-    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, _stream(stream))
-    _check(st, "swa_kv4_cache_append")
+    at = _Args(k_new, "k_new")
+    B, Hkv, d = shape = k_new.shape
+    kp, vp = at(k_new, "k_new", torch.bfloat16, shape), at(v_new, "v_new", torch.bfloat16, shape)
+    pp = at(pos, "pos", torch.int32, (B,))
+    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, at.stream(stream))
+    if st:
+        _check(st, "swa_kv4_cache_append")
 
 
 def swa_kv4_cache_read(positions, kcache, vcache, sink_k, sink_v, k_out, v_out, window: int, n_sink: int,
@@ -439,21 +461,25 @@ def swa_kv4_cache_read(positions, kcache, vcache, sink_k, sink_v, k_out, v_out, 
     """The values of cached positions (int32 [B, n]) into k_out/v_out [B, n, Hkv, d] (both bf16 or both float32)."""
     import torch
     _need(k_out.dim() == 4 and k_out.dtype in (torch.bfloat16, torch.float32), "k_out [B, n, Hkv, d] bf16 or float32")
-    B, n, Hkv, d = k_out.shape
-    ko, vo = _gpu(k_out, "k_out", k_out.dtype, k_out.shape), _gpu(v_out, "v_out", k_out.dtype, k_out.shape)
-    pp = _gpu(positions, "positions", torch.int32, (B, n))
-    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    code = SWA_DTYPE_F32 if k_out.dtype == torch.float32 else SWA_DTYPE_BF16
-    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, _stream(stream))
-    _check(st, "swa_kv4_cache_read")
+    at = _Args(k_out, "k_out")
+    B, n, Hkv, d = shape = k_out.shape
+    ko, vo = at(k_out, "k_out", k_out.dtype, shape), at(v_out, "v_out", k_out.dtype, shape)
+    pp = at(positions, "positions", torch.int32, (B, n))
+    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    code = SWA_DTYPE_F32 if k_out.dtype is torch.float32 else SWA_DTYPE_BF16
+    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, at.stream(stream))
+    if st:
+        _check(st, "swa_kv4_cache_read")
 
 
 def _decode_io(q, out, lse):
     import torch
-    _need(q.dim() == 3 and out.dtype in (torch.bfloat16, torch.float32), "q [B, Hq, d], out bf16 or float32")
-    return (_gpu(q, "q", torch.bfloat16, q.shape), _gpu(out, "out", out.dtype, q.shape),
-            None if lse is None else _gpu(lse, "lse", torch.float32, q.shape[:2]),
-            SWA_DTYPE_BF16_F32OUT if out.dtype == torch.float32 else SWA_DTYPE_BF16)
+    code = {torch.bfloat16: SWA_DTYPE_BF16, torch.float32: SWA_DTYPE_BF16_F32OUT}.get(out.dtype)
+    _need(q.dim() == 3 and code is not None, "q [B, Hq, d], out bf16 or float32")
+    at = _Args(q, "q")
+    shape = q.shape
+    return (at, at(q, "q", torch.bfloat16, shape), at(out, "out", out.dtype, shape),
+            None if lse is None else at(lse, "lse", torch.float32, shape[:2]), code)
 
 
 def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int, n_sink: int, scale=None,
@@ -461,15 +487,16 @@ def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int
     """One decode step over the 4-bit ring cache; q [B, Hq, d] bf16 at positions pos (int32 [B]);
     writes out [B, Hq, d] (bf16 or float32) and lse [B, Hq] (or None).  No workspace."""
     import torch
-    qp, op, lp, code = _decode_io(q, out, lse)
+    at, qp, op, lp, code = _decode_io(q, out, lse)
     B, Hq, d = q.shape
     _need(kcache.dim() == 4, "kcache [B, Hkv, window, row]")
     Hkv = kcache.shape[1]
-    pp = _gpu(pos, "pos", torch.int32, (B,))
-    cache = _kv4_cache(kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    pp = at(pos, "pos", torch.int32, (B,))
+    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
     st = _load().swa_kv4_decode(qp, *cache, pp, op, lp, B, Hq, Hkv, d, window, n_sink, _scale(scale, d), code,
-                                _stream(stream))
-    _check(st, "swa_kv4_decode")
+                                at.stream(stream))
+    if st:
+        _check(st, "swa_kv4_decode")
 
 
 def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=None, stream=None) -> None:
@@ -477,22 +504,24 @@ def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=
     k [B, L, Hkv, d] bf16 and lse [B, Hq, L] as swa_fwd takes and leaves them; writes score [B, Hkv, L] float32."""
     import torch
     _need(q.dim() == 4 and k.dim() == 4, "q [B, L, Hq, d], k [B, L, Hkv, d]")
+    at = _Args(q, "q")
     B, L, Hq, d = q.shape
     Hkv = k.shape[2]
-    st = _load().swa_hh_scores(_gpu(q, "q", torch.bfloat16, q.shape), _gpu(k, "k", torch.bfloat16, (B, L, Hkv, d)),
-                               _gpu(lse, "lse", torch.float32, (B, Hq, L)),
-                               _gpu(score, "score", torch.float32, (B, Hkv, L)), B, Hq, Hkv, L, d, n_obs, window,
-                               n_sink, _scale(scale, d), _stream(stream))
-    _check(st, "swa_hh_scores")
+    st = _load().swa_hh_scores(at(q, "q", torch.bfloat16, q.shape), at(k, "k", torch.bfloat16, (B, L, Hkv, d)),
+                               at(lse, "lse", torch.float32, (B, Hq, L)),
+                               at(score, "score", torch.float32, (B, Hkv, L)), B, Hq, Hkv, L, d, n_obs, window,
+                               n_sink, _scale(scale, d), at.stream(stream))
+    if st:
+        _check(st, "swa_hh_scores")
 
 
-def _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d):
+def _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d):
     import torch
     _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
     C = kcache.shape[2]
-    return C, (_gpu(kcache, "kcache", torch.bfloat16, (B, Hkv, C, d)),
-               _gpu(vcache, "vcache", torch.bfloat16, (B, Hkv, C, d)),
-               _gpu(slot_pos, "slot_pos", torch.int32, (B, Hkv, C)), _gpu(score, "score", torch.float32, (B, Hkv, C)))
+    rows, slots = (B, Hkv, C, d), (B, Hkv, C)
+    return C, (at(kcache, "kcache", torch.bfloat16, rows), at(vcache, "vcache", torch.bfloat16, rows),
+               at(slot_pos, "slot_pos", torch.int32, slots), at(score, "score", torch.float32, slots))
 
 
 def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: int, recent: int, stream=None) -> None:
@@ -500,12 +529,14 @@ def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: i
     [B, L, Hkv, d] (bf16), weights score_in [B, Hkv, L], in a cache of capacity kcache.shape[2]."""
     import torch
     _need(k.dim() == 4, "k [B, L, Hkv, d]")
-    B, L, Hkv, d = k.shape
-    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_cache_fill(_gpu(k, "k", torch.bfloat16, k.shape), _gpu(v, "v", torch.bfloat16, k.shape),
-                                   _gpu(score_in, "score_in", torch.float32, (B, Hkv, L)), L, *cache, B, Hkv, d, C,
-                                   n_sink, recent, _stream(stream))
-    _check(st, "swa_hh_cache_fill")
+    at = _Args(k, "k")
+    B, L, Hkv, d = shape = k.shape
+    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_fill(at(k, "k", torch.bfloat16, shape), at(v, "v", torch.bfloat16, shape),
+                                   at(score_in, "score_in", torch.float32, (B, Hkv, L)), L, *cache, B, Hkv, d, C,
+                                   n_sink, recent, at.stream(stream))
+    if st:
+        _check(st, "swa_hh_cache_fill")
 
 
 def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot, n_sink: int, recent: int,
@@ -514,36 +545,39 @@ def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot
     an empty slot, or the lightest slot that may be evicted; slot int32 [B, Hkv] (or None) receives which."""
     import torch
     _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
-    B, Hkv, d = k_new.shape
-    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_cache_append(_gpu(k_new, "k_new", torch.bfloat16, k_new.shape),
-                                     _gpu(v_new, "v_new", torch.bfloat16, k_new.shape),
-                                     _gpu(pos, "pos", torch.int32, (B,)), *cache,
-                                     None if slot is None else _gpu(slot, "slot", torch.int32, (B, Hkv)), B, Hkv, d, C,
-                                     n_sink, recent, _stream(stream))
-    _check(st, "swa_hh_cache_append")
+    at = _Args(k_new, "k_new")
+    B, Hkv, d = shape = k_new.shape
+    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_append(at(k_new, "k_new", torch.bfloat16, shape),
+                                     at(v_new, "v_new", torch.bfloat16, shape), at(pos, "pos", torch.int32, (B,)),
+                                     *cache, None if slot is None else at(slot, "slot", torch.int32, (B, Hkv)), B, Hkv,
+                                     d, C, n_sink, recent, at.stream(stream))
+    if st:
+        _check(st, "swa_hh_cache_append")
 
 
 def swa_hh_decode(q, kcache, vcache, slot_pos, score, out, lse, scale=None, decay: float = 1.0, stream=None) -> None:
     """One decode step over the occupied slots; q [B, Hq, d] bf16; writes out [B, Hq, d] (bf16 or float32)
     and lse [B, Hq] (or None), and sets score = decay * score + the slot's softmax weights."""
-    qp, op, lp, code = _decode_io(q, out, lse)
+    at, qp, op, lp, code = _decode_io(q, out, lse)
     B, Hq, d = q.shape
     _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
     Hkv = kcache.shape[1]
-    C, cache = _hh_cache(kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), float(decay), code,
-                               _stream(stream))
-    _check(st, "swa_hh_decode")
+    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), decay, code, at.stream(stream))
+    if st:
+        _check(st, "swa_hh_decode")
 
 
-def _rope_rows(t, name: str, T: int, d: int):
+def _rope_rows(t, name: str, T: int, d: int, dev: int):
     """Address, heads and token stride of t [T, H, d]; its heads lie contiguously, its tokens may be apart."""
-    import torch
-    _need(t.is_cuda and t.get_device() == torch.cuda.current_device(), f"{name}: CUDA tensor on the current device")
-    _need(t.dim() == 3 and t.shape[0] == T and t.shape[2] == d and t.stride(2) == 1 and t.stride(1) == d,
-          f"{name} [T, H, d] with contiguous heads")
-    return t.data_ptr(), t.shape[1], t.stride(0) if T > 1 else t.shape[1] * d
+    if t.get_device() != dev or t.dim() != 3:
+        raise ValueError(f"{name} [T, H, d] on the current CUDA device")
+    rows, H, n = t.shape
+    # a dimension of one element has no stride to speak of
+    if rows != T or n != d or t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} [{T}, H, {d}] with contiguous heads")
+    return t.data_ptr(), H, t.stride(0) if T > 1 else H * d
 
 
 def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_base: float = 10000.0,
@@ -553,20 +587,23 @@ def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_b
     "interleaved".  The tokens of q and k may be strided views.  inverse=True turns back (the backward pass)."""
     import torch
     _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float32), "q [T, Hq, d] bf16 or float32")
-    _need(layout in _ROPE_LAYOUTS, f"layout one of {sorted(_ROPE_LAYOUTS)}")
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout one of {sorted(_ROPE_LAYOUTS)}")
+    at = _Args(q, "q")
     T, _, d = q.shape
-    qp, Hq, qs = _rope_rows(q, "q", T, d)
+    qp, Hq, qs = _rope_rows(q, "q", T, d, at.dev)
     kp, Hkv, ks = None, 0, 0
     if k is not None:
-        _need(k.dtype == q.dtype, "k of q's type")
-        kp, Hkv, ks = _rope_rows(k, "k", T, d)
+        _need(k.dtype is q.dtype, "k of q's type")
+        kp, Hkv, ks = _rope_rows(k, "k", T, d, at.dev)
     n_axes = len(sections)
-    pp = _gpu(positions, "positions", torch.int32, (n_axes, T))
+    pp = at(positions, "positions", torch.int32, (n_axes, T))
     sec = (ctypes.c_int32 * max(1, n_axes))(*sections)
     st = _load().swa_rope_axes_qk(qp, kp, pp, T, Hq, Hkv, d, qs, ks, sec, n_axes, _ROPE_LAYOUTS[layout],
-                                  float(rope_base), int(bool(inverse)),
-                                  SWA_DTYPE_F32 if q.dtype == torch.float32 else SWA_DTYPE_BF16, _stream(stream))
-    _check(st, "swa_rope_axes_qk")
+                                  rope_base, 1 if inverse else 0,
+                                  SWA_DTYPE_F32 if q.dtype is torch.float32 else SWA_DTYPE_BF16, at.stream(stream))
+    if st:
+        _check(st, "swa_rope_axes_qk")
 
 
 def swa_hadamard_proj(y, alpha, beta, z, stream=None) -> None:

@@ -54,45 +54,64 @@ __device__ __forceinline__ void mma_bf16_16816(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B (no accumulator to clear first).
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Partial softmax state of the heads of one KV head.  The sums are relative to
 // 2^ref: O = sum 2^(z - ref) v, l = sum 2^(z - ref); ref = -inf and l = 0 without keys.
 template <int D>
-struct Partial {
+struct alignas(16) Partial {
   float o[kDecHeads][D];
   float ref[kDecHeads];
   float l[kDecHeads];
 };
 
-// Weights of n partial states with references r[i] and sums l[i], and the total.
-__device__ __forceinline__ float merge_ref(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ float merge_weight(float ref, float top) {
-  return ref == -INFINITY ? 0.f : exp2f(ref - top);
+  return ref == -INFINITY ? 0.f : ex2_approx(ref - top);
+}
+__device__ __forceinline__ float4 axpy4(float a, float4 x, float4 y) {
+  return make_float4(fmaf(a, x.x, y.x), fmaf(a, x.y, y.y), fmaf(a, x.z, y.z), fmaf(a, x.w, y.w));
 }
 
 // Combine the warps' states (in shared memory, warp w's at part(w)) into `mine`, then
-// the cluster's: rank r of `c` blocks writes its share of the output rows of segment
-// `seg_head0` (index of the first query head).  On return lse2[h] (shared memory) is the
-// log2 of the segment's sum of 2^z, -inf without keys.
+// the cluster's: rank r of `c` blocks writes its share of the output rows, head0 being
+// the index of the segment's first query head.  Four elements a thread throughout, the
+// weights once per thread and head.  On return lse2[h] (shared memory) is the log2 of
+// the segment's sum of 2^z, -inf without keys.
 template <int D, typename PartOf>
 __device__ __forceinline__ void merge_and_store(PartOf part, Partial<D>* mine, float* lse2, int G, int c, int rank,
-                                                size_t seg_head0, void* out, bool out_f32, float* lse) {
+                                                size_t head0, void* out, bool out_f32, float* lse) {
   namespace cg = cooperative_groups;
   const int tid = threadIdx.x;
   constexpr int kThreads = kDecWarps * 32;
+  constexpr int V = D / 4;  // float4s of a row
   __syncthreads();
-  for (int i = tid; i < G * D; i += kThreads) {
-    const int h = i / D, e = i % D;
-    float top = -INFINITY;
+  for (int i = tid; i < G * V; i += kThreads) {
+    const int h = i / V, e = i % V;
+    float w[kDecWarps], top = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, part(w)->ref[h]);
-    float acc = 0.f, l = 0.f;
+    for (int k = 0; k < kDecWarps; ++k) top = fmaxf(top, w[k] = part(k)->ref[h]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float a = merge_weight(part(w)->ref[h], top);
-      acc += a * part(w)->o[h][e];
-      l += a * part(w)->l[h];
+    for (int k = 0; k < kDecWarps; ++k) {
+      const float a = merge_weight(w[k], top);
+      acc = axpy4(a, reinterpret_cast<const float4*>(part(k)->o[h])[e], acc);
+      l = fmaf(a, part(k)->l[h], l);
     }
-    mine->o[h][e] = acc;
+    reinterpret_cast<float4*>(mine->o[h])[e] = acc;
     if (e == 0) {
       mine->ref[h] = top;
       mine->l[h] = l;
@@ -100,35 +119,36 @@ __device__ __forceinline__ void merge_and_store(PartOf part, Partial<D>* mine, f
   }
   cg::cluster_group cluster = cg::this_cluster();
   if (c > 1) cluster.sync(); else __syncthreads();
-  for (int i = rank * kThreads + tid; i < G * D; i += c * kThreads) {
-    const int h = i / D, e = i % D;
-    float top = -INFINITY;
+  // this rank's float4s, and every head's log-sum-exp
+  const int share = (G * V + c - 1) / c;
+  for (int i = tid; i < share + kDecHeads; i += kThreads) {
+    const bool row = i < share;
+    const int at = rank * share + i;
+    const int h = row ? at / V : i - share, e = row ? at % V : 0;
+    if (h >= G) continue;
+    float top = -INFINITY, l = 0.f;
     for (int r = 0; r < c; ++r) top = fmaxf(top, cluster.map_shared_rank(mine, r)->ref[h]);
-    float acc = 0.f, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < c; ++r) {
       const Partial<D>* p = cluster.map_shared_rank(mine, r);
       const float a = merge_weight(p->ref[h], top);
-      acc += a * p->o[h][e];
-      l += a * p->l[h];
+      if (row) acc = axpy4(a, reinterpret_cast<const float4*>(p->o[h])[e], acc);
+      l = fmaf(a, p->l[h], l);
     }
-    const float y = l > 0.f ? acc / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
-    const size_t at = (seg_head0 + h) * D + e;
-    if (out_f32)
-      static_cast<float*>(out)[at] = y;
-    else
-      static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(y);
-  }
-  if (tid < G) {
-    const int h = tid;
-    float top = -INFINITY, l = 0.f;
-    for (int r = 0; r < c; ++r) top = fmaxf(top, cluster.map_shared_rank(mine, r)->ref[h]);
-    for (int r = 0; r < c; ++r) {
-      const Partial<D>* p = cluster.map_shared_rank(mine, r);
-      l += merge_weight(p->ref[h], top) * p->l[h];
+    if (row) {
+      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no keys: zeros; a NaN sum stays one
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      const size_t o = (head0 + h) * D + 4 * e;
+      if (out_f32)
+        *reinterpret_cast<float4*>(static_cast<float*>(out) + o) = acc;
+      else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + o) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    } else {
+      const float s = l == 0.f ? -INFINITY : top + log2f(l);
+      lse2[h] = s;
+      if (rank == 0 && lse != nullptr) lse[head0 + h] = s * 0.69314718055994531f;
     }
-    const float s = l == 0.f ? -INFINITY : top + log2f(l);
-    lse2[h] = s;
-    if (rank == 0 && lse != nullptr) lse[seg_head0 + h] = s * 0.69314718055994531f;
   }
   // no block leaves, or reuses its shared memory, while another one reads it
   if (c > 1) cluster.sync(); else __syncthreads();

@@ -77,12 +77,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
   float* s_z = reinterpret_cast<float*>(smem + kDecWarps * kStages * C::STAGE);  // [local tile][G][16]
   const int nw = c * kDecWarps;
 
-  // Occupied rows of a tile, as bits; the lanes of a half warp read one slot each.
-  auto occupied = [&](int tile) -> unsigned {
+  // Positions in a tile's slots, one per lane of a half warp, and the occupied ones as bits.
+  // They are read a tile before the tile is requested, so that nothing waits for them.
+  auto slots_of = [&](int tile) -> int {
     const int i = tile * kDecTile + (lane & 15);
-    const bool occ = tile < tiles && i < cap && sp[i] >= 0;
-    return __ballot_sync(kFull, occ) & 0xffffu;
+    return tile < tiles && i < cap ? sp[i] : -1;
   };
+  auto occupied = [&](int at) -> unsigned { return __ballot_sync(kFull, at >= 0) & 0xffffu; };
   auto issue = [&](int tile, int stage, unsigned mask) {
     if (mask != 0) {
       const uint8_t* ks = kc + static_cast<size_t>(tile) * kDecTile * (D * 2);
@@ -103,11 +104,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
   };
 
   int tile = rank * kDecWarps + warp;
-  unsigned masks[kStages];  // of the tiles tile, tile + nw, ...; the last one is not issued yet
+  unsigned masks[kStages];  // of the tiles tile, tile + nw, ...
+  int ahead;                // slots of the first tile that has no mask yet
+  {
+    int at[kStages];
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) masks[s] = occupied(tile + s * nw);
+    for (int s = 0; s < kStages; ++s) at[s] = slots_of(tile + s * nw);
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(tile + s * nw, s, masks[s]);
+    for (int s = 0; s < kStages - 1; ++s) {
+      masks[s] = occupied(at[s]);
+      issue(tile + s * nw, s, masks[s]);
+    }
+    ahead = at[kStages - 1];
+  }
 
   // ---- q: row g of A is head g
   uint32_t qa[C::KS][2];
@@ -133,10 +142,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     cp_async_wait<kStages - 2>();
     __syncwarp();
     const unsigned mask = masks[0];
+    masks[kStages - 1] = occupied(ahead);
+    ahead = slots_of(tile + kStages * nw);
     issue(tile + (kStages - 1) * nw, stage == 0 ? kStages - 1 : stage - 1, masks[kStages - 1]);
 #pragma unroll
     for (int s = 0; s + 1 < kStages; ++s) masks[s] = masks[s + 1];
-    masks[kStages - 1] = occupied(tile + kStages * nw);
     if (mask != 0) {
       const uint8_t* kt = ring + stage * C::STAGE;
       const uint8_t* vt = kt + C::HALF;

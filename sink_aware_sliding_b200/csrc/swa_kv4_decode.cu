@@ -26,41 +26,33 @@ namespace swa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kStages = 4;
+constexpr int kStages = 2;
+constexpr int kRows = 32;  // keys per tile: two products of 16 rows share a step of the softmax
+constexpr int kBlocksPerSm = 4;
 
 template <int D>
 struct K4 {
   static constexpr int NG = D / kKv4Group;
   static constexpr int ROW = kv4_row_bytes(D);
   static constexpr int CODES = D / 2;                    // code bytes of a row
-  static constexpr int PAR = 4 * NG;                     // parameter bytes of a row
   static constexpr int UNIT = D == 128 ? 16 : 8;         // bytes per copy: what a row is aligned to
-  static constexpr int UNITS = ROW / UNIT;               // 5
-  static constexpr int COPIES = (kDecTile * UNITS + 31) / 32;  // per lane, for K and again for V
-  static constexpr int HALF = kDecTile * ROW;            // K's or V's bytes of a stage
+  static constexpr int UNITS = ROW / UNIT;               // 5: as many copies per lane for 32 rows
+  static constexpr int HALF = kRows * ROW;               // K's or V's bytes of a stage, rows as in the cache
   static constexpr int STAGE = 2 * HALF;
+  static constexpr int SCORES = kRows * kDecHeads * 4;   // a warp's score tile, turned through shared memory
+  static constexpr int WARP = kStages * STAGE + SCORES;
 };
-
-// Key rows of a tile that lane (g, t) multiplies: t, 4 + (t ^ X) and those + 8.  X and
-// the order of the 16-byte chunks in shared memory (chunk c of row r at c ^ (r & 2) for
-// d = 128) keep both the K reads (two rows per quarter warp) and the V reads (four rows)
-// off each other's banks.
-template <int D>
-__device__ __forceinline__ int row_lo(int n) {  // token of column n of a score tile
-  constexpr int X = D == 128 ? 1 : 2;
-  return (n & 1) ? 4 + ((n >> 1) ^ X) : n >> 1;
-}
-template <int D>
-__device__ __forceinline__ int code_at(int r, int byte) {  // where byte of row r's codes lies in a tile
-  if constexpr (D == 128) return r * 64 + ((((byte >> 4) ^ (r & 2)) << 4) | (byte & 15));
-  return r * 32 + byte;
-}
 
 __device__ __forceinline__ float step_of(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_f16(lo, hi);
 }
 
 template <int NW>
@@ -76,9 +68,15 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[NW], const uint8_t* p) {
   }
 }
 
+// Exponent bits of a group's step, or of its |minimum| less 24 where that is more (a group
+// of one value), as those of a bf16.
+__device__ __forceinline__ int size_of(uint32_t w) {
+  return max(static_cast<int>(w & 0x7fffu), static_cast<int>((w >> 16) & 0x7fffu) - (24 << 7));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs a,
-                                                                          int c) {
+__global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
+    swa_kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs a, int c) {
   using C = K4<D>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -95,60 +93,58 @@ __global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const
   const int p = a.pos[b];
   const int n_ring = p < 0 ? 0 : (p < W ? p + 1 : W);
   const int n_sink = p < W ? 0 : min(p - W + 1, S);
-  const int ring_tiles = (n_ring + kDecTile - 1) / kDecTile;
-  const int tiles = ring_tiles + (n_sink + kDecTile - 1) / kDecTile;
-  const uint8_t* kc = a.kc + seg * W * C::ROW;
-  const uint8_t* vc = a.vc + seg * W * C::ROW;
-  const uint8_t* sk = a.sk + seg * S * C::ROW;
-  const uint8_t* sv = a.sv + seg * S * C::ROW;
-
-  uint8_t* ring = smem + warp * (kStages * C::STAGE);
-  const uint32_t ring_u32 = smem_u32(ring);
-  // where this lane's copies go within a half stage
-  int copy_row[C::COPIES];
-  uint32_t copy_dst[C::COPIES];
-#pragma unroll
-  for (int i = 0; i < C::COPIES; ++i) {
-    const int u = lane + 32 * i;
-    const int r = u / C::UNITS, byte = (u % C::UNITS) * C::UNIT;
-    copy_row[i] = u < kDecTile * C::UNITS ? r : kDecTile;  // kDecTile: none
-    copy_dst[i] = byte < C::CODES ? code_at<D>(r, byte) : kDecTile * C::CODES + r * C::PAR + byte - C::CODES;
-  }
+  const int ring_tiles = (n_ring + kRows - 1) / kRows;
+  const int tiles = ring_tiles + (n_sink + kRows - 1) / kRows;
+  // A tile's copies: unit lane + 32 i, i < 5, of K's rows and of V's is this lane's.
+  const size_t ring0 = seg * W * C::ROW, sink0 = seg * S * C::ROW;
+  uint8_t* mine = smem + warp * C::WARP;
+  const uint32_t ring_u32 = smem_u32(mine);
+  const int full_tiles = n_ring / kRows;
+  const int nw = c * kDecWarps;
+  int tile = rank * kDecWarps + warp;
+  // where this lane reads the next whole ring tile from
+  const uint8_t* ks = a.kc + ring0 + static_cast<size_t>(tile) * C::HALF + lane * C::UNIT;
+  const uint8_t* vs = a.vc + ring0 + static_cast<size_t>(tile) * C::HALF + lane * C::UNIT;
+  const size_t ks_step = static_cast<size_t>(nw) * C::HALF;
   auto issue = [&](int tile, int stage) {
-    if (tile < tiles) {
-      const bool in_ring = tile < ring_tiles;
-      const int first = (in_ring ? tile : tile - ring_tiles) * kDecTile;
-      const int n = min(kDecTile, (in_ring ? n_ring : n_sink) - first);
-      const uint8_t* ks = (in_ring ? kc : sk) + static_cast<size_t>(first) * C::ROW;
-      const uint8_t* vs = (in_ring ? vc : sv) + static_cast<size_t>(first) * C::ROW;
-      const uint32_t dst = ring_u32 + stage * C::STAGE;
+    const uint32_t dst = ring_u32 + stage * C::STAGE + lane * C::UNIT;
+    if (tile < full_tiles) {
 #pragma unroll
-      for (int i = 0; i < C::COPIES; ++i) {
-        if (copy_row[i] < kDecTile) {
-          const bool real = copy_row[i] < n;
-          const int off = real ? (lane + 32 * i) * C::UNIT : 0;
-          cp_async<C::UNIT>(dst + copy_dst[i], ks + off, real);
-          cp_async<C::UNIT>(dst + C::HALF + copy_dst[i], vs + off, real);
-        }
+      for (int i = 0; i < C::UNITS; ++i) {
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, ks + 32 * i * C::UNIT, true);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, vs + 32 * i * C::UNIT, true);
+      }
+      ks += ks_step;
+      vs += ks_step;
+    } else if (tile < tiles) {  // the ring's last rows, or sinks; rows behind the last one become zeros
+      const bool in_ring = tile < ring_tiles;
+      const int first = (in_ring ? tile : tile - ring_tiles) * kRows;
+      const int n = (in_ring ? n_ring : n_sink) - first;
+      const size_t at = (in_ring ? ring0 : sink0) + static_cast<size_t>(first) * C::ROW + lane * C::UNIT;
+      const uint8_t* k1 = (in_ring ? a.kc : a.sk) + at;
+      const uint8_t* v1 = (in_ring ? a.vc : a.sv) + at;
+#pragma unroll
+      for (int i = 0; i < C::UNITS; ++i) {
+        const bool real = lane + 32 * i < n * C::UNITS;
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, real ? k1 + 32 * i * C::UNIT : a.kc, real);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, real ? v1 + 32 * i * C::UNIT : a.vc, real);
       }
     }
     cp_async_commit();
   };
 
-  const int nw = c * kDecWarps;
-  int tile = rank * kDecWarps + warp;
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) issue(tile + s * nw, s);
 
-  // ---- q of head g: fp16 fragments scaled by 2^-qe, and the sums of its groups
-  uint32_t qa[NG][4];
-  float qsum[NG];
-  float qscale;
+  // ---- q of head g: fp16 fragments scaled by a power of two, and the sums of its groups
+  uint32_t qb[NG][4];
+  uint32_t qs0, qs1;  // sum of group t in three bf16 parts: what multiplies the minima
+  float qscale0, qscale1;
   {
     const bool real = g < G;
     const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + (head0 + (real ? g : 0)) * D;
     float x[NG][8];
-    float mx = 0.f;
+    float mx = 0.f, sum_t = 0.f;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const uint4 w = real ? *reinterpret_cast<const uint4*>(qrow + 32 * j + 8 * t) : make_uint4(0, 0, 0, 0);
@@ -163,96 +159,112 @@ __global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const
       }
       sum += __shfl_xor_sync(kFull, sum, 1);
       sum += __shfl_xor_sync(kFull, sum, 2);
-      qsum[j] = sum * a.scale_log2;
+      if (j == t) sum_t = sum * a.scale_log2;
     }
+    const float hi = __bfloat162float(__float2bfloat16_rn(sum_t));
+    const float mid = __bfloat162float(__float2bfloat16_rn(sum_t - hi));
+    qs0 = pack_bf16x2(hi, mid);
+    qs1 = pack_bf16x2(sum_t - hi - mid, 0.f);
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
     // largest element to [2^14, 2^15)
     int e = static_cast<int>(__float_as_uint(mx) >> 23) - 127;
     e = min(max(e, -100), 100) - 14;
     const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    qscale = __uint_as_float(static_cast<uint32_t>(127 + e + 12) << 23) * (a.scale_log2 * 4096.f);  // 2^(e + 24)
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e + 12) << 23) * (a.scale_log2 * 4096.f);  // 2^(e + 24)
+    qscale0 = __shfl_sync(kFull, up, 8 * t);  // of heads 2t and 2t + 1
+    qscale1 = __shfl_sync(kFull, up, 8 * t + 4);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       // k-slots of the two products: nibbles (0, 2), then (1, 3), which carry a factor 16
-      qa[j][0] = pack_f16(x[j][0] * down, x[j][4] * down);
-      qa[j][1] = pack_f16(x[j][2] * down, x[j][6] * down);
-      qa[j][2] = pack_f16(x[j][1] * down * 0.0625f, x[j][5] * down * 0.0625f);
-      qa[j][3] = pack_f16(x[j][3] * down * 0.0625f, x[j][7] * down * 0.0625f);
+      qb[j][0] = pack_f16(x[j][0] * down, x[j][4] * down);
+      qb[j][1] = pack_f16(x[j][2] * down, x[j][6] * down);
+      qb[j][2] = pack_f16(x[j][1] * down * 0.0625f, x[j][5] * down * 0.0625f);
+      qb[j][3] = pack_f16(x[j][3] * down * 0.0625f, x[j][7] * down * 0.0625f);
     }
   }
 
   float o[NG][2][4];
-  float omin[NG];
+  float om[4] = {0.f, 0.f, 0.f, 0.f};  // minima's part: row g is group g; [0] head 2t, [1] head 2t + 1
 #pragma unroll
-  for (int j = 0; j < NG; ++j) {
-    omin[j] = 0.f;
+  for (int j = 0; j < NG; ++j)
 #pragma unroll
     for (int x = 0; x < 2; ++x) o[j][x][0] = o[j][x][1] = o[j][x][2] = o[j][x][3] = 0.f;
-  }
   float ref = -INFINITY, l = 0.f;
-  const int row_n = row_lo<D>(g);                           // K: this lane's token of a score tile (and + 8)
-  const int r0 = row_lo<D>(2 * t), r1 = row_lo<D>(2 * t + 1);  // scores and V: this lane's tokens (and + 8)
+  // Scores: rows g and g + 8 of the product are the tokens kr and kr + 8; P and V: this
+  // lane's tokens are 2t, 2t + 1 and those + 8.  In rows of 80 bytes both orders keep the
+  // reads off each other's banks (K: two rows per quarter warp, V: four per half warp).
+  const int kr = (g >> 1) + 4 * (g & 1);
+  const int kcode = kr * C::ROW + t * (C::CODES / 4), kpar = kr * C::ROW + C::CODES;
+  const int vcode = 2 * t * C::ROW + g * 2 * NG, vpar = 2 * t * C::ROW + C::CODES;
+  float* scores = reinterpret_cast<float*>(mine + kStages * C::STAGE);
 
   int stage = 0;
   for (; tile < tiles; tile += nw) {
     cp_async_wait<kStages - 2>();
     __syncwarp();  // this tile has arrived for every lane, and every lane is done with the one before
     issue(tile + (kStages - 1) * nw, stage == 0 ? kStages - 1 : stage - 1);
-    const uint8_t* kt = ring + stage * C::STAGE;
+    const uint8_t* kt = mine + stage * C::STAGE;
     const uint8_t* vt = kt + C::HALF;
-    const uint8_t* kp = kt + kDecTile * C::CODES;
-    const uint8_t* vp = vt + kDecTile * C::CODES;
-    const bool in_ring = tile < ring_tiles;
-    const int n = (in_ring ? n_ring : n_sink) - (in_ring ? tile : tile - ring_tiles) * kDecTile;
 
-    // ---- scores of head g for the tokens r0, r1, r0 + 8, r1 + 8
-    float z[4];
+    // ---- scores of the tokens kr, kr + 8 of each 16 for the heads 2t, 2t + 1
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      uint32_t w[NG];
-      lds_words<NG>(w, kt + code_at<D>(row_n + 8 * nt, t * (C::CODES / 4)));
-      uint32_t pa[NG], pb[NG];
-      lds_words<NG>(pa, kp + (r0 + 8 * nt) * C::PAR);
-      lds_words<NG>(pb, kp + (r1 + 8 * nt) * C::PAR);
-      float za = 0.f, zb = 0.f, ma = 0.f, mb = 0.f;
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t wa[NG], wb[NG], pa[NG], pb[NG];
+      lds_words<NG>(wa, kt + 16 * hf * C::ROW + kcode);
+      lds_words<NG>(wb, kt + 16 * hf * C::ROW + kcode + 8 * C::ROW);
+      lds_words<NG>(pa, kt + 16 * hf * C::ROW + kpar);
+      lds_words<NG>(pb, kt + 16 * hf * C::ROW + kpar + 8 * C::ROW);
+      const uint32_t ma = *reinterpret_cast<const uint32_t*>(kt + 16 * hf * C::ROW + kpar + t % NG * 4);
+      const uint32_t mb = *reinterpret_cast<const uint32_t*>(kt + 16 * hf * C::ROW + kpar + t % NG * 4 + 8 * C::ROW);
+      float low[4];  // minimum of group t in every k-slot, times the sums of q
+      const uint32_t a0 = __byte_perm(ma, ma, 0x3232), a1 = __byte_perm(mb, mb, 0x3232);
+      mma_bf16_zero(low, a0, a1, a0, a1, qs0, qs1);
+      float z0 = 0.f, z1 = 0.f, z2 = 0.f, z3 = 0.f;
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         // elements 8 t + i (low half) and 8 t + 4 + i of group j
-        const uint32_t x = __byte_perm(w[j >> 1], w[(j >> 1) + NG / 2], (j & 1) ? 0x7632 : 0x5410);
-        const uint32_t y = x >> 8;
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16_16816(acc, qa[j][0], 0u, qa[j][1], 0u, x & 0x000f000fu, y & 0x000f000fu);
-        mma_f16_16816(acc, qa[j][2], 0u, qa[j][3], 0u, x & 0x00f000f0u, y & 0x00f000f0u);
-        za = fmaf(step_of(pa[j]), acc[0], za);
-        zb = fmaf(step_of(pb[j]), acc[1], zb);
-        ma = fmaf(low_of(pa[j]), qsum[j], ma);
-        mb = fmaf(low_of(pb[j]), qsum[j], mb);
+        const uint32_t x = __byte_perm(wa[j >> 1], wa[(j >> 1) + NG / 2], (j & 1) ? 0x7632 : 0x5410);
+        const uint32_t y = __byte_perm(wb[j >> 1], wb[(j >> 1) + NG / 2], (j & 1) ? 0x7632 : 0x5410);
+        const uint32_t xh = x >> 8, yh = y >> 8;
+        float acc[4];
+        mma_f16_zero(acc, x & 0x000f000fu, y & 0x000f000fu, xh & 0x000f000fu, yh & 0x000f000fu, qb[j][0], qb[j][1]);
+        mma_f16_16816(acc, x & 0x00f000f0u, y & 0x00f000f0u, xh & 0x00f000f0u, yh & 0x00f000f0u, qb[j][2], qb[j][3]);
+        const float sa = step_of(pa[j]), sb = step_of(pb[j]);
+        z0 = fmaf(sa, acc[0], z0);
+        z1 = fmaf(sa, acc[1], z1);
+        z2 = fmaf(sb, acc[2], z2);
+        z3 = fmaf(sb, acc[3], z3);
       }
-      z[2 * nt] = fmaf(za, qscale, ma);
-      z[2 * nt + 1] = fmaf(zb, qscale, mb);
+      *reinterpret_cast<float2*>(scores + (kr + 16 * hf) * kDecHeads + 2 * t) =
+          make_float2(fmaf(z0, qscale0, low[0]), fmaf(z1, qscale1, low[1]));
+      *reinterpret_cast<float2*>(scores + (kr + 8 + 16 * hf) * kDecHeads + 2 * t) =
+          make_float2(fmaf(z2, qscale0, low[2]), fmaf(z3, qscale1, low[3]));
     }
-    if (n < kDecTile) {
-      if (r0 >= n) z[0] = -INFINITY;
-      if (r1 >= n) z[1] = -INFINITY;
-      if (r0 + 8 >= n) z[2] = -INFINITY;
-      if (r1 + 8 >= n) z[3] = -INFINITY;
+    __syncwarp();
+    // ---- turned: head g, tokens 2t, 2t + 1 and those + 8, 16, 24
+    float z[8];
+    auto token = [&](int i) { return 2 * t + (i & 1) + (i >> 1) * 8; };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = scores[token(i) * kDecHeads + g];
+    if (tile >= full_tiles) {
+      const bool in_ring = tile < ring_tiles;
+      const int n = (in_ring ? n_ring : n_sink) - (in_ring ? tile : tile - ring_tiles) * kRows;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (token(i) >= n) z[i] = -INFINITY;
     }
     // ---- reference: p times the tile's largest step stays within fp16
-    float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    float mx = max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), fmaxf(z[6], z[7]));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    // exponent of the tile's largest step, or of its largest |minimum| less 24 where that is
-    // more (groups of one value), as bf16 bits
-    auto size_of = [](uint32_t w) {
-      return max(static_cast<int>(w & 0x7fffu), static_cast<int>((w >> 16) & 0x7fffu) - (24 << 7));
-    };
     int big;
-    if constexpr (D == 128) {
-      const uint2 w = *reinterpret_cast<const uint2*>(vp + lane * 8);
-      big = max(size_of(w.x), size_of(w.y));
-    } else {
-      big = size_of(*reinterpret_cast<const uint32_t*>(vp + lane * 4));
+    {
+      uint32_t w[NG];
+      lds_words<NG>(w, vt + lane * C::ROW + C::CODES);
+      big = size_of(w[0]);
+#pragma unroll
+      for (int j = 1; j < NG; ++j) big = max(big, size_of(w[j]));
     }
     big = __reduce_max_sync(kFull, big);
     const int be = min(max((big >> 7) - 127, -90), 100);
@@ -264,43 +276,59 @@ __global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const
       const float a0 = __shfl_sync(kFull, alpha, 8 * t), a1 = __shfl_sync(kFull, alpha, 8 * t + 4);
       ref = next;
       l *= alpha;
+      om[0] *= a0;
+      om[1] *= a1;
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        omin[j] *= alpha;
+      for (int j = 0; j < NG; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           o[j][x][0] *= a0; o[j][x][1] *= a1; o[j][x][2] *= a0; o[j][x][3] *= a1;
         }
-      }
     }
     const float base = ref == -INFINITY ? 0.f : ref;
-    float pr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(z[i] - base);
-    l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+    for (int i = 0; i < 8; ++i) z[i] = ex2_approx(z[i] - base);
+    l += ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
 
-    // ---- O += P V
-    uint32_t va[NG / 2], vb[NG / 2], vc2[NG / 2], vd[NG / 2];
-    lds_words<NG / 2>(va, vt + code_at<D>(r0, g * 2 * NG));
-    lds_words<NG / 2>(vb, vt + code_at<D>(r1, g * 2 * NG));
-    lds_words<NG / 2>(vc2, vt + code_at<D>(r0 + 8, g * 2 * NG));
-    lds_words<NG / 2>(vd, vt + code_at<D>(r1 + 8, g * 2 * NG));
-    uint32_t p0[NG], p1[NG], p2[NG], p3[NG];
-    lds_words<NG>(p0, vp + r0 * C::PAR);
-    lds_words<NG>(p1, vp + r1 * C::PAR);
-    lds_words<NG>(p2, vp + (r0 + 8) * C::PAR);
-    lds_words<NG>(p3, vp + (r1 + 8) * C::PAR);
+    // ---- O += P V, 16 tokens at a time
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-      omin[j] += (pr[0] * low_of(p0[j]) + pr[1] * low_of(p1[j])) + (pr[2] * low_of(p2[j]) + pr[3] * low_of(p3[j]));
-      const uint32_t b0 = pack_f16(pr[0] * step_of(p0[j]), pr[1] * step_of(p1[j]));
-      const uint32_t b1 = pack_f16(pr[2] * step_of(p2[j]), pr[3] * step_of(p3[j]));
-      // elements 4 g + i of group j: tokens r0 (low half) and r1
-      const uint32_t x = __byte_perm(va[j >> 1], vb[j >> 1], (j & 1) ? 0x7632 : 0x5410);
-      const uint32_t y = __byte_perm(vc2[j >> 1], vd[j >> 1], (j & 1) ? 0x7632 : 0x5410);
-      const uint32_t xh = x >> 8, yh = y >> 8;
-      mma_f16_16816(o[j][0], x & 0x000f000fu, xh & 0x000f000fu, y & 0x000f000fu, yh & 0x000f000fu, b0, b1);
-      mma_f16_16816(o[j][1], x & 0x00f000f0u, xh & 0x00f000f0u, y & 0x00f000f0u, yh & 0x00f000f0u, b0, b1);
+    for (int hf = 0; hf < 2; ++hf) {
+      const uint8_t* v0 = vt + 16 * hf * C::ROW;
+      uint32_t p0[NG], p1[NG], p2[NG], p3[NG];
+      lds_words<NG>(p0, v0 + vpar);
+      lds_words<NG>(p1, v0 + vpar + C::ROW);
+      lds_words<NG>(p2, v0 + vpar + 8 * C::ROW);
+      lds_words<NG>(p3, v0 + vpar + 9 * C::ROW);
+      {
+        // the minima times P in two bf16 parts: row g of the product is group g % NG, and so is row g + 8
+        const uint8_t* q = v0 + vpar + g % NG * 4;
+        const uint32_t m0 = __byte_perm(*reinterpret_cast<const uint32_t*>(q),
+                                        *reinterpret_cast<const uint32_t*>(q + C::ROW), 0x7632);
+        const uint32_t m1 = __byte_perm(*reinterpret_cast<const uint32_t*>(q + 8 * C::ROW),
+                                        *reinterpret_cast<const uint32_t*>(q + 9 * C::ROW), 0x7632);
+        const uint32_t h0 = pack_bf16x2(z[4 * hf], z[4 * hf + 1]), h1 = pack_bf16x2(z[4 * hf + 2], z[4 * hf + 3]);
+        const uint32_t l0 = pack_bf16x2(z[4 * hf] - step_of(h0), z[4 * hf + 1] - low_of(h0));
+        const uint32_t l1 = pack_bf16x2(z[4 * hf + 2] - step_of(h1), z[4 * hf + 3] - low_of(h1));
+        mma_bf16_16816(om, m0, m0, m1, m1, h0, h1);
+        mma_bf16_16816(om, m0, m0, m1, m1, l0, l1);
+      }
+      uint32_t va[NG / 2], vb[NG / 2], vc[NG / 2], vd[NG / 2];
+      lds_words<NG / 2>(va, v0 + vcode);
+      lds_words<NG / 2>(vb, v0 + vcode + C::ROW);
+      lds_words<NG / 2>(vc, v0 + vcode + 8 * C::ROW);
+      lds_words<NG / 2>(vd, v0 + vcode + 9 * C::ROW);
+      const uint64_t pr0 = f2_pack(z[4 * hf], z[4 * hf + 1]), pr1 = f2_pack(z[4 * hf + 2], z[4 * hf + 3]);
+  #pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const uint32_t b0 = pack_f16(f2_mul(pr0, f2_pack(step_of(p0[j]), step_of(p1[j]))));
+        const uint32_t b1 = pack_f16(f2_mul(pr1, f2_pack(step_of(p2[j]), step_of(p3[j]))));
+        // elements 4 g + i of group j: tokens 2t (low half) and 2t + 1
+        const uint32_t x = __byte_perm(va[j >> 1], vb[j >> 1], (j & 1) ? 0x7632 : 0x5410);
+        const uint32_t y = __byte_perm(vc[j >> 1], vd[j >> 1], (j & 1) ? 0x7632 : 0x5410);
+        const uint32_t xh = x >> 8, yh = y >> 8;
+        mma_f16_16816(o[j][0], x & 0x000f000fu, xh & 0x000f000fu, y & 0x000f000fu, yh & 0x000f000fu, b0, b1);
+        mma_f16_16816(o[j][1], x & 0x00f000f0u, xh & 0x00f000f0u, y & 0x00f000f0u, yh & 0x00f000f0u, b0, b1);
+      }
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
@@ -309,16 +337,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const
 
   // ---- this warp's state, in its own (now idle) stages
   static_assert(sizeof(Partial<D>) <= kStages * C::STAGE, "a partial state fits a warp's stages");
-  auto part = [&](int w) { return reinterpret_cast<Partial<D>*>(smem + w * (kStages * C::STAGE)); };
+  auto part = [&](int w) { return reinterpret_cast<Partial<D>*>(smem + w * C::WARP); };
   Partial<D>* pt = part(warp);
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
-    float m = omin[j];
-    m += __shfl_xor_sync(kFull, m, 1);
-    m += __shfl_xor_sync(kFull, m, 2);
-    const float m0 = __shfl_sync(kFull, m, 8 * t), m1 = __shfl_sync(kFull, m, 8 * t + 4);
+    const float m0 = __shfl_sync(kFull, om[0], 4 * j + t), m1 = __shfl_sync(kFull, om[1], 4 * j + t);
     constexpr float kEven = 16777216.f, kOdd = 1048576.f;  // 2^24, 2^20
     if (2 * t < G)
       *reinterpret_cast<float4*>(&pt->o[2 * t][32 * j + 4 * g]) =
@@ -338,12 +363,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 4) swa_kv4_decode_kernel(const
 
 template <int D>
 cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
-  const size_t smem = kDecWarps * kStages * K4<D>::STAGE;
+  const size_t smem = kDecWarps * K4<D>::WARP;
   const long long segments = static_cast<long long>(a.B) * a.Hkv;
-  const long long tiles = (static_cast<long long>(a.W) + a.S + kDecTile - 1) / kDecTile;
-  const int c = decode_cluster(segments, tiles, sms, 4, 2);
+  const long long tiles = (static_cast<long long>(a.W) + a.S + kRows - 1) / kRows;
+  const int c = decode_cluster(segments, tiles, sms, kBlocksPerSm, 1);
   if (segments * c > INT32_MAX) return cudaErrorInvalidValue;
-  static_assert(kDecWarps * kStages * K4<D>::STAGE <= 48 * 1024, "no opt-in shared memory needed");
+  cudaError_t e = cudaFuncSetAttribute(swa_kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
   cfg.blockDim = dim3(kDecWarps * 32);
