@@ -70,6 +70,21 @@ __device__ __forceinline__ void mma_bf16_zero(float (&c)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Four 8 x 8 matrices of 16-bit elements, the rows of matrix i at the addresses of lanes 8 i .. 8 i + 7: what
+// one m16n8k16 product takes as A, or, transposed on the way, what it takes from a tile stored the other way.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 // Partial softmax state of the heads of one KV head.  The sums are relative to
 // 2^ref: O = sum 2^(z - ref) v, l = sum 2^(z - ref); ref = -inf and l = 0 without keys.
 template <int D>

@@ -1,13 +1,16 @@
 // Decode over the cache that evicts by accumulated attention weight: softmax attention
 // over the occupied slots, and each slot's weight added to its score, in one launch.
 //
-// Bound by HBM like the ring cache's decode: every row is read once.  S = Q K^T and
-// O^T += V^T P^T run as mma.sync m16n8k16 on bf16 rows, as they are; P is split into
-// two bf16 parts (hi + lo, 2^-17 relative together) at the price of a second product,
-// since the weights are a result of their own here.  The scaled scores stay in shared
-// memory (4 bytes a slot and query head, spread over the cluster's blocks), so that
-// when the cluster has merged its sums, each block turns its slots' scores into
-// weights and adds them up without a second pass over K.
+// Bound by HBM like the ring cache's decode: every row is read once.  S^T = K Q^T and
+// O^T += V^T P^T run as mma.sync m16n8k16 on bf16 rows as they are, the tokens (then the
+// elements) as the 16 rows of a product and up to eight query heads as its columns;
+// ldmatrix delivers both operands, V's transposed on the way.  P is split into two bf16
+// parts (hi + lo, 2^-17 relative together) at the price of a second product, since the
+// weights are a result of their own here.  The scaled scores stay in shared memory
+// (4 bytes a slot and query head, spread over the cluster's blocks), where they are also
+// turned from the first product's layout to the second's; when the cluster has merged
+// its sums, each block makes weights of its slots' scores and adds them up, without a
+// second pass over K.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,32 +36,14 @@ struct HB {
   static constexpr int MT = D / 16;                            // row tiles of O^T
 };
 
-// Unit u of row r lies at u ^ swz(r): the K reads of a quarter warp (rows q, q + 4, four
-// neighbouring units) and the V reads (rows 0..3 or 4..7, two units) each fall on all
-// 32 banks once.
-__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) ^ (r & 4); }
-
-// Blocks per cluster, and the shared memory of its blocks.
-template <int D>
-struct HhPlan {
-  int c;
-  size_t smem;
-};
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-// bf16 element e of a (low half) and of b
-__device__ __forceinline__ uint32_t pair_of(const uint4& a, const uint4& b, int e) {
-  return __byte_perm(word_of(a, e >> 1), word_of(b, e >> 1), (e & 1) ? 0x7632 : 0x5410);
-}
+// Unit u of row r lies at u ^ (r & 7), so that the eight rows of a matrix that ldmatrix
+// reads lie in different banks.
 
 template <int D>
 __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const __grid_constant__ HhDecodeArgs a,
                                                                          int c) {
   using C = HB<D>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Partial<D> s_mine;
   __shared__ float s_lse2[kDecHeads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -74,7 +59,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
 
   uint8_t* ring = smem + warp * (kStages * C::STAGE);
   const uint32_t ring_u32 = smem_u32(ring);
-  float* s_z = reinterpret_cast<float*>(smem + kDecWarps * kStages * C::STAGE);  // [local tile][G][16]
+  float* s_z = reinterpret_cast<float*>(smem + kDecWarps * kStages * C::STAGE);  // [local tile][16][G]
   const int nw = c * kDecWarps;
 
   // Positions in a tile's slots, one per lane of a half warp, and the occupied ones as bits.
@@ -95,7 +80,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
         const int r = u / C::UNITS, unit = u % C::UNITS;
         const bool real = (mask >> r) & 1;
         const int off = real ? u * 16 : 0;
-        const uint32_t at = (r * C::UNITS + (unit ^ swz(r & 7))) * 16;
+        const uint32_t at = (r * C::UNITS + (unit ^ (r & 7))) * 16;
         cp_async<16>(dst + at, ks + off, real);
         cp_async<16>(dst + C::HALF + at, vs + off, real);
       }
@@ -118,24 +103,27 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     ahead = at[kStages - 1];
   }
 
-  // ---- q: row g of A is head g
-  uint32_t qa[C::KS][2];
+  // ---- q: column g of B is head g
+  uint32_t qb[C::KS][2];
   {
     const bool real = g < G;
-    const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + (head0 + (real ? g : 0)) * D;
+    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                             (head0 + (real ? g : 0)) * D);
 #pragma unroll
-    for (int s = 0; s < C::KS / 2; ++s) {
-      const uint4 w = real ? *reinterpret_cast<const uint4*>(qrow + s * 32 + t * 8) : make_uint4(0, 0, 0, 0);
-      qa[2 * s][0] = w.x; qa[2 * s][1] = w.y;
-      qa[2 * s + 1][0] = w.z; qa[2 * s + 1][1] = w.w;
+    for (int s = 0; s < C::KS; ++s) {
+      qb[s][0] = real ? qrow[8 * s + t] : 0u;
+      qb[s][1] = real ? qrow[8 * s + 4 + t] : 0u;
     }
   }
   float o[C::MT][4];
 #pragma unroll
   for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float ref = -INFINITY, l = 0.f;
-  const int row_n = (g & 1) ? 4 + (g >> 1) : g >> 1;  // K: this lane's row of a score tile (and + 8)
-  const int r0 = t, r1 = t + 4;                       // scores and V: this lane's rows (and + 8)
+  // This lane's row of the matrices that ldmatrix reads.  K: matrices (rows 0-7, 8-15) x (unit
+  // 2s, 2s + 1); V: (unit 2i, 2i + 1) x (rows 0-7, 8-15), transposed.
+  const int km_row = lane & 15, km_unit = lane >> 4;
+  const int vm_row = (lane & 7) + ((lane >> 4) << 3), vm_unit = (lane >> 3) & 1;
+  const uint32_t km_at = km_row * C::UNITS * 16, vm_at = C::HALF + vm_row * C::UNITS * 16;
 
   int stage = 0, local = warp;
   for (; tile < tiles; tile += nw, local += kDecWarps) {
@@ -148,29 +136,28 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
 #pragma unroll
     for (int s = 0; s + 1 < kStages; ++s) masks[s] = masks[s + 1];
     if (mask != 0) {
-      const uint8_t* kt = ring + stage * C::STAGE;
-      const uint8_t* vt = kt + C::HALF;
-      float z[4];
+      const uint32_t tile_u32 = ring_u32 + stage * C::STAGE;
+      float acc[2][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int s = 0; s < C::KS / 2; ++s) {
-          const uint4 w = *reinterpret_cast<const uint4*>(
-              kt + ((row_n + 8 * nt) * C::UNITS + ((4 * s + t) ^ swz(row_n))) * 16);
-          mma_bf16_16816(acc[0], qa[2 * s][0], 0u, qa[2 * s][1], 0u, w.x, w.y);
-          mma_bf16_16816(acc[1], qa[2 * s + 1][0], 0u, qa[2 * s + 1][1], 0u, w.z, w.w);
-        }
-        z[2 * nt] = (acc[0][0] + acc[1][0]) * a.scale_log2;
-        z[2 * nt + 1] = (acc[0][1] + acc[1][1]) * a.scale_log2;
+      for (int s = 0; s < C::KS; ++s) {
+        uint32_t k4[4];
+        ldmatrix_x4(k4, tile_u32 + km_at + (((2 * s + km_unit) ^ (km_row & 7)) << 4));
+        if (s < 2)
+          mma_bf16_zero(acc[s], k4[0], k4[1], k4[2], k4[3], qb[s][0], qb[s][1]);
+        else
+          mma_bf16_16816(acc[s & 1], k4[0], k4[1], k4[2], k4[3], qb[s][0], qb[s][1]);
       }
-      const int rows[4] = {r0, r1, r0 + 8, r1 + 8};
+      // rows g, g + 8 and heads 2t, 2t + 1, to be read back as head g and rows 2t, 2t + 1 and those + 8
+      float* zt = s_z + static_cast<size_t>(local) * kDecTile * G;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (!((mask >> rows[i]) & 1)) z[i] = -INFINITY;
-      if (g < G) {
+        if (2 * t + (i & 1) < G) zt[(g + (i >> 1) * 8) * G + 2 * t + (i & 1)] = (acc[0][i] + acc[1][i]) * a.scale_log2;
+      __syncwarp();
+      float z[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_z[(local * G + g) * kDecTile + rows[i]] = z[i];
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+        z[i] = g < G && ((mask >> row) & 1) ? zt[row * G + g] : -INFINITY;
       }
       float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
@@ -194,21 +181,12 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
       const uint32_t h0 = pack_bf16x2(pr[0], pr[1]), h1 = pack_bf16x2(pr[2], pr[3]);
       const uint32_t l0 = pack_bf16x2(pr[0] - __uint_as_float(h0 << 16), pr[1] - __uint_as_float(h0 & 0xffff0000u));
       const uint32_t l1 = pack_bf16x2(pr[2] - __uint_as_float(h1 << 16), pr[3] - __uint_as_float(h1 & 0xffff0000u));
-      uint4 v[4][C::UNITS / 8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int u = 0; u < C::UNITS / 8; ++u)
-          v[i][u] = *reinterpret_cast<const uint4*>(vt + (rows[i] * C::UNITS + ((8 * u + g) ^ swz(rows[i] & 7))) * 16);
 #pragma unroll
       for (int mt = 0; mt < C::MT; ++mt) {
-        // row g: element mt of unit g; row g + 8: of unit 8 + g (d = 128) or element 4 + mt (d = 64)
-        const int e2 = D == 128 ? mt : 4 + mt;
-        constexpr int u2 = D == 128 ? 1 : 0;
-        const uint32_t v0 = pair_of(v[0][0], v[1][0], mt), v1 = pair_of(v[0][u2], v[1][u2], e2);
-        const uint32_t v2 = pair_of(v[2][0], v[3][0], mt), v3 = pair_of(v[2][u2], v[3][u2], e2);
-        mma_bf16_16816(o[mt], v0, v1, v2, v3, h0, h1);
-        mma_bf16_16816(o[mt], v0, v1, v2, v3, l0, l1);
+        uint32_t v4[4];
+        ldmatrix_x4_trans(v4, tile_u32 + vm_at + (((2 * mt + vm_unit) ^ (vm_row & 7)) << 4));
+        mma_bf16_16816(o[mt], v4[0], v4[1], v4[2], v4[3], h0, h1);
+        mma_bf16_16816(o[mt], v4[0], v4[1], v4[2], v4[3], l0, l1);
       }
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -216,14 +194,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
   cp_async_wait<0>();
   __syncwarp();
 
-  static_assert(sizeof(Partial<D>) <= kStages * C::STAGE, "a partial state fits a warp's stages");
+  static_assert(2 * sizeof(Partial<D>) <= kStages * C::STAGE, "a warp's state and the block's fit a warp's stages");
   auto part = [&](int w) { return reinterpret_cast<Partial<D>*>(smem + w * (kStages * C::STAGE)); };
   Partial<D>* pt = part(warp);
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt) {
-    const int dA = g * 8 + mt, dB = D == 128 ? 64 + g * 8 + mt : g * 8 + 4 + mt;
+    const int dA = 16 * mt + g, dB = dA + 8;
     if (2 * t < G) {
       pt->o[2 * t][dA] = o[mt][0];
       pt->o[2 * t][dB] = o[mt][2];
@@ -237,7 +215,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     pt->ref[g] = ref;
     pt->l[g] = l;
   }
-  merge_and_store<D>(part, &s_mine, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
+  merge_and_store<D>(part, part(0) + 1, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
 
   // ---- weights of this block's slots: block tile i is tile rank * kDecWarps + (i % kDecWarps) + (i / kDecWarps) * nw
   __syncthreads();
@@ -245,13 +223,25 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
   const int mine = tiles > rank * kDecWarps
                        ? (tiles - rank * kDecWarps + nw - 1) / nw * kDecWarps  // upper bound; checked below
                        : 0;
-  for (int i = threadIdx.x; i < mine * kDecTile; i += kDecWarps * 32) {
-    const int lt = i / kDecTile, r = i % kDecTile;
-    const int slot = (rank * kDecWarps + lt % kDecWarps + lt / kDecWarps * nw) * kDecTile + r;
-    if (slot < cap && sp[slot] >= 0) {
+  constexpr int kBatch = 4;  // slots a thread has in flight
+  for (int i0 = threadIdx.x; i0 < mine * kDecTile; i0 += kBatch * kDecWarps * 32) {
+    int slot[kBatch], at[kBatch];
+    float old[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kDecWarps * 32, lt = i / kDecTile;
+      slot[k] = (rank * kDecWarps + lt % kDecWarps + lt / kDecWarps * nw) * kDecTile + i % kDecTile;
+      const bool real = i < mine * kDecTile && slot[k] < cap;
+      at[k] = real ? sp[slot[k]] : -1;
+      old[k] = real ? sc[slot[k]] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (at[k] < 0) continue;
+      const float* z = s_z + static_cast<size_t>(i0 + k * kDecWarps * 32) * G;
       float w = 0.f;
-      for (int h = 0; h < G; ++h) w += ex2_approx(s_z[(lt * G + h) * kDecTile + r] - s_lse2[h]);
-      sc[slot] = fmaf(a.decay, sc[slot], w);
+      for (int h = 0; h < G; ++h) w += ex2_approx(z[h] - s_lse2[h]);
+      sc[slot[k]] = fmaf(a.decay, old[k], w);
     }
   }
 }
@@ -267,8 +257,8 @@ cudaError_t launch_impl(const HhDecodeArgs& a, int sms, cudaStream_t stream) {
     const long long local = (tiles + n * kDecWarps - 1) / (n * kDecWarps) * kDecWarps;
     return kRing + static_cast<size_t>(local) * a.G * kDecTile * 4;
   };
-  constexpr size_t kMost = 220 * 1024;  // of 227 KB; the merge's static part is below 5 KB
-  while (c < 8 && smem_of(c) > kMost) c *= 2;
+  constexpr size_t kMost = 226 * 1024, kTwo = 112 * 1024;  // one block's on an SM, and each of two blocks'
+  while (c < 8 && smem_of(c) > kTwo) c *= 2;
   const size_t smem = smem_of(c);
   if (smem > kMost || segments * c > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(swa_hh_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,

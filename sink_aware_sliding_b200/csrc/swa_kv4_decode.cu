@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   using C = K4<D>;
   constexpr int NG = C::NG;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Partial<D> s_mine;
   __shared__ float s_lse2[kDecHeads];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   __syncwarp();
 
   // ---- this warp's state, in its own (now idle) stages
-  static_assert(sizeof(Partial<D>) <= kStages * C::STAGE, "a partial state fits a warp's stages");
+  static_assert(2 * sizeof(Partial<D>) <= kStages * C::STAGE, "a warp's state and the block's fit a warp's stages");
   auto part = [&](int w) { return reinterpret_cast<Partial<D>*>(smem + w * C::WARP); };
   Partial<D>* pt = part(warp);
   l += __shfl_xor_sync(kFull, l, 1);
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
     pt->ref[g] = ref;
     pt->l[g] = l;
   }
-  merge_and_store<D>(part, &s_mine, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
+  merge_and_store<D>(part, part(0) + 1, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
 }
 
 template <int D>
