@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     return tile < tiles && i < cap ? sp[i] : -1;
   };
   auto occupied = [&](int at) -> unsigned { return __ballot_sync(kFull, at >= 0) & 0xffffu; };
+  const uint64_t policy = stream_policy();
   auto issue = [&](int tile, int stage, unsigned mask) {
     if (mask != 0) {
       const uint8_t* ks = kc + static_cast<size_t>(tile) * kDecTile * (D * 2);
@@ -81,8 +82,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
         const bool real = (mask >> r) & 1;
         const int off = real ? u * 16 : 0;
         const uint32_t at = (r * C::UNITS + (unit ^ (r & 7))) * 16;
-        cp_async<16>(dst + at, ks + off, real);
-        cp_async<16>(dst + C::HALF + at, vs + off, real);
+        cp_async<16>(dst + at, ks + off, real, policy);
+        cp_async<16>(dst + C::HALF + at, vs + off, real, policy);
       }
     }
     cp_async_commit();
@@ -102,6 +103,33 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     }
     ahead = at[kStages - 1];
   }
+
+  // ---- this block's slots: block tile i is tile rank * kDecWarps + i % kDecWarps + i / kDecWarps * nw.  The
+  // first ones' positions and scores are read here, long before they are wanted, and stay in registers.
+  const int first_tile = rank * kDecWarps;
+  const int mine = tiles > first_tile ? (tiles - first_tile + nw - 1) / nw * kDecWarps * kDecTile : 0;  // or fewer
+  float* sc = a.score + seg * cap;
+  constexpr int kBatch = 8;  // slots a thread has in flight
+  constexpr int kThreads = kDecWarps * 32;
+  auto slot_at = [&](int i) {
+    const int lt = i / kDecTile;
+    return (first_tile + lt % kDecWarps + lt / kDecWarps * nw) * kDecTile + i % kDecTile;
+  };
+  int at_pos[kBatch];
+  float old[kBatch];
+  auto read_scores = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kThreads;
+      const int at = slot_at(i);
+      at_pos[k] = -1;
+      if (i < mine && at < cap) {
+        old[k] = sc[at];
+        at_pos[k] = sp[at];
+      }
+    }
+  };
+  read_scores(threadIdx.x);
 
   // ---- q: column g of B is head g
   uint32_t qb[C::KS][2];
@@ -216,34 +244,33 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     pt->l[g] = l;
   }
   merge_and_store<D>(part, part(0) + 1, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
-
-  // ---- weights of this block's slots: block tile i is tile rank * kDecWarps + (i % kDecWarps) + (i / kDecWarps) * nw
-  __syncthreads();
-  float* sc = a.score + seg * cap;
-  const int mine = tiles > rank * kDecWarps
-                       ? (tiles - rank * kDecWarps + nw - 1) / nw * kDecWarps  // upper bound; checked below
-                       : 0;
-  constexpr int kBatch = 4;  // slots a thread has in flight
-  for (int i0 = threadIdx.x; i0 < mine * kDecTile; i0 += kBatch * kDecWarps * 32) {
-    int slot[kBatch], at[kBatch];
-    float old[kBatch];
+  float top[kDecHeads];
+#pragma unroll
+  for (int h = 0; h < kDecHeads; ++h) top[h] = h < G ? s_lse2[h] : 0.f;
+  for (int i0 = threadIdx.x; i0 < mine; i0 += kBatch * kThreads) {
+    if (i0 != threadIdx.x) read_scores(i0);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kDecWarps * 32, lt = i / kDecTile;
-      slot[k] = (rank * kDecWarps + lt % kDecWarps + lt / kDecWarps * nw) * kDecTile + i % kDecTile;
-      const bool real = i < mine * kDecTile && slot[k] < cap;
-      at[k] = real ? sp[slot[k]] : -1;
-      old[k] = real ? sc[slot[k]] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (at[k] < 0) continue;
-      const float* z = s_z + static_cast<size_t>(i0 + k * kDecWarps * 32) * G;
+      if (at_pos[k] < 0) continue;
+      const float* z = s_z + static_cast<size_t>(i0 + k * kThreads) * G;
       float w = 0.f;
-      for (int h = 0; h < G; ++h) w += ex2_approx(z[h] - s_lse2[h]);
-      sc[slot[k]] = fmaf(a.decay, old[k], w);
+      if ((G & 3) == 0) {
+#pragma unroll
+        for (int h = 0; h < kDecHeads; h += 4)
+          if (h < G) {
+            const float4 x = *reinterpret_cast<const float4*>(z + h);
+            w += (ex2_approx(x.x - top[h]) + ex2_approx(x.y - top[h + 1])) +
+                 (ex2_approx(x.z - top[h + 2]) + ex2_approx(x.w - top[h + 3]));
+          }
+      } else {
+#pragma unroll
+        for (int h = 0; h < kDecHeads; ++h)
+          if (h < G) w += ex2_approx(z[h] - top[h]);
+      }
+      sc[slot_at(i0 + k * kThreads)] = fmaf(a.decay, old[k], w);
     }
   }
+  merge_done(c);
 }
 
 template <int D>

@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "hh_scores.h"
 #include "prefill_common.cuh"
@@ -217,30 +218,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                            (t0 + 127 <= x.j0 + a.pa.window - 1 || x.j0 + 127 < a.pa.n_sink);
         const int c_lo = j - t0, c_hi = last - t0;
         float part[4] = {0.f, 0.f, 0.f, 0.f};
+        // two loops, so that a tile without an edge has no comparisons
+        auto add = [&](auto edge) {
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t r[32];
-          tmem_ld32_wait(tmem + 128 * sb + lane_off + c0, r);
-          if (c0 == 96) {
-            tc_fence_before();
-            mbar_arrive(s_empty + 8 * sb);
-          }
+          for (int c0 = 0; c0 < 128; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32_wait(tmem + 128 * sb + lane_off + c0, r);
+            if (c0 == 96) {
+              tc_fence_before();
+              mbar_arrive(s_empty + 8 * sb);
+            }
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(lse + c0 + c);
-            float e[4];
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2, f2_pack(w.x, w.y)), e[0],
-                      e[1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2, f2_pack(w.z, w.w)),
-                      e[2], e[3]);
+            for (int c = 0; c < 32; c += 4) {
+              const float4 w = *reinterpret_cast<const float4*>(lse + c0 + c);
+              float e[4];
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), sl2, f2_pack(w.x, w.y)),
+                        e[0], e[1]);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])), sl2,
+                               f2_pack(w.z, w.w)),
+                        e[2], e[3]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float p = ex2_approx(e[q]);
-              if (!whole) p = (c0 + c + q >= c_lo && c0 + c + q <= c_hi) ? p : 0.f;
-              part[q] += p;
+              for (int q = 0; q < 4; ++q) {
+                float p = ex2_approx(e[q]);
+                if constexpr (decltype(edge)::value) p = (c0 + c + q >= c_lo && c0 + c + q <= c_hi) ? p : 0.f;
+                part[q] += p;
+              }
             }
           }
-        }
+        };
+        if (whole)
+          add(std::false_type{});
+        else
+          add(std::true_type{});
         total += static_cast<double>((part[0] + part[1]) + (part[2] + part[3]));
       }
       if (!ok) break;

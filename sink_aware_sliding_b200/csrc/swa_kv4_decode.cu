@@ -105,13 +105,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   const uint8_t* ks = a.kc + ring0 + static_cast<size_t>(tile) * C::HALF + lane * C::UNIT;
   const uint8_t* vs = a.vc + ring0 + static_cast<size_t>(tile) * C::HALF + lane * C::UNIT;
   const size_t ks_step = static_cast<size_t>(nw) * C::HALF;
+  const uint64_t policy = stream_policy();
   auto issue = [&](int tile, int stage) {
     const uint32_t dst = ring_u32 + stage * C::STAGE + lane * C::UNIT;
     if (tile < full_tiles) {
 #pragma unroll
       for (int i = 0; i < C::UNITS; ++i) {
-        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, ks + 32 * i * C::UNIT, true);
-        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, vs + 32 * i * C::UNIT, true);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, ks + 32 * i * C::UNIT, true, policy);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, vs + 32 * i * C::UNIT, true, policy);
       }
       ks += ks_step;
       vs += ks_step;
@@ -125,8 +126,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
 #pragma unroll
       for (int i = 0; i < C::UNITS; ++i) {
         const bool real = lane + 32 * i < n * C::UNITS;
-        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, real ? k1 + 32 * i * C::UNIT : a.kc, real);
-        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, real ? v1 + 32 * i * C::UNIT : a.vc, real);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT, real ? k1 + 32 * i * C::UNIT : a.kc, real, policy);
+        cp_async<C::UNIT>(dst + 32 * i * C::UNIT + C::HALF, real ? v1 + 32 * i * C::UNIT : a.vc, real, policy);
       }
     }
     cp_async_commit();
@@ -358,6 +359,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
     pt->l[g] = l;
   }
   merge_and_store<D>(part, part(0) + 1, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
+  merge_done(c);
 }
 
 template <int D>
