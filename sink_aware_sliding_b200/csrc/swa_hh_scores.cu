@@ -6,8 +6,8 @@
 // (sequence, KV head), its K tile is loaded once, and the tiles of 128 observing queries
 // of each head stream past it.  S^T = K Q^T runs on tcgen05 with the keys as the 128
 // TMEM lanes: a thread owns one key and adds up its row of exponentials, without any
-// exchange between threads.  Four S tiles in TMEM and two warpgroups that take every
-// other tile keep the exponentials, which bound the kernel (16 a cycle and SM against
+// exchange between threads.  Four S tiles in TMEM and four warpgroups that take every
+// fourth tile keep the exponentials, which bound the kernel (16 a cycle and SM against
 // 4096 multiply-adds: at d = 128 twice the product's time), from waiting for products.
 // Sums: float32 over a tile's 128 columns in four chains, float64 over the tiles.
 #include <cuda.h>
@@ -27,8 +27,9 @@ namespace {
 using prefill::Ctl;
 using prefill::wait_bar;
 
-constexpr int kThreads = 320;  // two warpgroups of exponentials, a load warp, an MMA warp
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kGroups = 4;     // warpgroups of exponentials
+constexpr int kThreads = 128 * kGroups + 64;  // and a load warp, an MMA warp
+constexpr int kLoadWarp = 4 * kGroups, kMmaWarp = kLoadWarp + 1;
 constexpr int kBuf = 4;        // S tiles in TMEM
 constexpr int kQStages = 3;
 
@@ -38,9 +39,9 @@ struct Cfg {
   static constexpr int NCHUNK = D / 64;                   // 128-byte columns of a tile
   static constexpr int OFF_K = 0;                         // two K tiles
   static constexpr int OFF_Q = 2 * TILE;
-  static constexpr int OFF_LSE = OFF_Q + kQStages * TILE;  // [8 warps][128] floats
-  static constexpr int OFF_SUM = OFF_LSE + 8 * 128 * 4;    // [128] doubles
-  static constexpr int OFF_BAR = OFF_SUM + 128 * 8;
+  static constexpr int OFF_LSE = OFF_Q + kQStages * TILE;   // [4 kGroups warps][128] floats
+  static constexpr int OFF_SUM = OFF_LSE + 4 * kGroups * 128 * 4;  // [kGroups - 1][128] doubles
+  static constexpr int OFF_BAR = OFF_SUM + (kGroups - 1) * 128 * 8;
   static constexpr int NBAR = 4 + 2 * kQStages + 2 * kBuf + 3;
   static constexpr int SMEM = OFF_BAR + 8 * NBAR + 16 + 1024;
 };
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full + 8 * i, 1);
       mbar_init(s_empty + 8 * i, 128);
     }
-    mbar_init(sum_full, 128);
+    mbar_init(sum_full, 128 * (kGroups - 1));
     mbar_init(sum_empty, 128);
     mbar_init(drain, 1);
     *ctl.abort_flag = 0;
@@ -191,33 +192,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sl2 = f2_pack(a.pa.scale_log2, a.pa.scale_log2);
     int n = 0, uc = 0;
     bool ok = true;
+    // lse of the next tile of this warpgroup, four columns a lane, on its way while the current
+    // tile is worked on (tile i of unit x)
+    float ahead[4];
+    auto fetch = [&](const Unit& x, int i) {
+      const int h = i / x.n_qt, t0 = t_first + (x.qt_lo + i - h * x.n_qt) * 128;
+      const float* src = a.lse + (static_cast<size_t>(x.b) * a.pa.Hq + x.kvh * G + h) * L + t0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) ahead[c] = t0 + lane + 32 * c < L ? src[lane + 32 * c] : 0.f;
+    };
+    Unit x = get_unit(a, blockIdx.x);  // the grid has no more blocks than units
+    if (wg < x.n_qt * G) fetch(x, wg);
     for (int u = blockIdx.x; ok && u < a.n_units; u += gridDim.x, ++uc) {
-      const Unit x = get_unit(a, u);
+      const Unit next = get_unit(a, min(u + static_cast<int>(gridDim.x), a.n_units - 1));
       const int j = x.j0 + row;
       // queries that see key j: [j, last]
       const int last = j >= L ? -1 : j < a.pa.n_sink ? L - 1 : min(L - 1, j + a.pa.window - 1);
       const int count = x.n_qt * G;
       double total = 0.0;
-      for (int i = 0; i < count; ++i, ++n) {
-        if ((n & 1) != wg) continue;
-        const int h = i / x.n_qt, qt = x.qt_lo + i - h * x.n_qt;
-        const int t0 = t_first + qt * 128;
-        {  // each warp keeps its own copy of the tile's -lse log2(e): no barrier between warps
-          const float* src = a.lse + (static_cast<size_t>(x.b) * a.pa.Hq + x.kvh * G + h) * L + t0;
-          __syncwarp();
+      // tiles of all units are numbered through; this warpgroup takes one of kGroups
+      const int first = (wg - n) & (kGroups - 1), first_next = (wg - n - count) & (kGroups - 1);
+      if (first >= count && first_next < next.n_qt * G) fetch(next, first_next);  // none here
+      for (int i = first; i < count; i += kGroups) {
+        const int t0 = t_first + (x.qt_lo + i % x.n_qt) * 128;
+        __syncwarp();
 #pragma unroll
-          for (int c = lane; c < 128; c += 32) lse[c] = t0 + c < L ? src[c] * -1.4426950408889634f : 0.f;
-          __syncwarp();
+        for (int c = 0; c < 4; ++c) lse[lane + 32 * c] = ahead[c] * -1.4426950408889634f;  // this warp's own copy
+        __syncwarp();
+        if (i + kGroups < count) {
+          fetch(x, i + kGroups);
+        } else if (first_next < next.n_qt * G) {
+          fetch(next, first_next);
         }
-        const int sb = n & (kBuf - 1);
-        ok = __all_sync(0xffffffffu, wait_bar(s_full + 8 * sb, (n / kBuf) & 1, ctl));
+        const int sb = (n + i) & (kBuf - 1);
+        ok = __all_sync(0xffffffffu, wait_bar(s_full + 8 * sb, ((n + i) / kBuf) & 1, ctl));
         if (!ok) break;
         tc_fence_after();
         // every key here sees every query of the tile?
         const bool whole = x.j0 + 127 <= t0 && t0 + 127 < L &&
                            (t0 + 127 <= x.j0 + a.pa.window - 1 || x.j0 + 127 < a.pa.n_sink);
         const int c_lo = j - t0, c_hi = last - t0;
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t part0 = 0, part1 = 0;  // two sums each
         // two loops, so that a tile without an edge has no comparisons
         auto add = [&](auto edge) {
 #pragma unroll
@@ -239,10 +254,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         e[2], e[3]);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                float p = ex2_approx(e[q]);
-                if constexpr (decltype(edge)::value) p = (c0 + c + q >= c_lo && c0 + c + q <= c_hi) ? p : 0.f;
-                part[q] += p;
+                e[q] = ex2_approx(e[q]);
+                if constexpr (decltype(edge)::value)
+                  e[q] = (c0 + c + q >= c_lo && c0 + c + q <= c_hi) ? e[q] : 0.f;
               }
+              part0 = f2_add(part0, f2_pack(e[0], e[1]));
+              part1 = f2_add(part1, f2_pack(e[2], e[3]));
             }
           }
         };
@@ -250,22 +267,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           add(std::false_type{});
         else
           add(std::true_type{});
-        total += static_cast<double>((part[0] + part[1]) + (part[2] + part[3]));
+        float s0, s1;
+        f2_unpack(f2_add(part0, part1), s0, s1);
+        total += static_cast<double>(s0 + s1);
       }
+      n += count;
       if (!ok) break;
-      // the two warpgroups' sums; bounded waits, so that an abort ends them too
-      if (wg == 1) {
+      // the warpgroups' sums; bounded waits, so that an abort ends them too
+      if (wg > 0) {
         ok = __all_sync(0xffffffffu, wait_bar(sum_empty, (uc & 1) ^ 1, ctl));
         if (!ok) break;
-        s_sum[row] = total;
+        s_sum[(wg - 1) * 128 + row] = total;
         mbar_arrive(sum_full);
       } else {
         ok = __all_sync(0xffffffffu, wait_bar(sum_full, uc & 1, ctl));
         if (!ok) break;
-        total += s_sum[row];
+#pragma unroll
+        for (int w = 0; w < kGroups - 1; ++w) total += s_sum[w * 128 + row];
         mbar_arrive(sum_empty);
         if (j < L) a.score[(static_cast<size_t>(x.b) * a.pa.Hkv + x.kvh) * L + j] = static_cast<float>(total);
       }
+      x = next;
     }
   }
 
