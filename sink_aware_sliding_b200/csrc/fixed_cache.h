@@ -6,6 +6,20 @@
 
 namespace swa {
 
+// Division of 0 <= n < 2^31 by a divisor known to the host, in three instructions: with
+// 2^l the power of two at or above d, q = (n + n * mul / 2^32) / 2^l, mul = 2^32 (2^l - d) / d + 1.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  explicit FastDiv(int divisor) : d(static_cast<uint32_t>(divisor)), shift(0) {
+    while (shift < 31 && (1u << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+  __device__ __forceinline__ uint32_t mod(uint32_t n) const { return n - div(n) * d; }
+#endif
+};
+
 // ---------------------------------------------------------------- 4-bit ring cache
 constexpr int kKv4Group = 32;  // elements that share a step and a minimum
 __host__ __device__ constexpr int kv4_row_bytes(int d) { return d / 2 + d / kKv4Group * 4; }

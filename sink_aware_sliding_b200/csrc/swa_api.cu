@@ -551,6 +551,8 @@ int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* 
   if (P < 0) return SWA_ERR_INVALID_ARG;
   if (P == 0 || B == 0) return SWA_OK;
   if (!k || !v || !aligned16(k) || !aligned16(v)) return SWA_ERR_INVALID_ARG;
+  if ((static_cast<long long>(std::min(P, window)) + std::min(P, n_sink)) * Hkv > INT32_MAX / 2)
+    return SWA_ERR_UNSUPPORTED;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != SWA_OK) return st;
   cudaError_t e = swa::launch_kv4_fill(k, v, P, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink, dev->sms,
@@ -578,6 +580,7 @@ int swa_kv4_cache_read(const int32_t* positions, int n, const void* kcache, cons
   if (st != SWA_OK) return st;
   if (n < 0 || (out_dtype != SWA_DTYPE_BF16 && out_dtype != SWA_DTYPE_F32)) return SWA_ERR_INVALID_ARG;
   if (n == 0 || B == 0) return SWA_OK;
+  if (static_cast<long long>(n) * Hkv > INT32_MAX / 2) return SWA_ERR_UNSUPPORTED;
   if (!positions || !aligned4(positions) || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
     return SWA_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;

@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "fixed_cache.h"
+#include "ptx.cuh"
 
 namespace swa {
 namespace {
@@ -48,16 +49,21 @@ __device__ __forceinline__ void quantise8(const uint4& x, uint32_t& piece0, uint
     step16 = __float2bfloat16_rn(0.f);
   }
   const float inv = step > 0.f ? __frcp_rn(step) : 0.f;
+  // (x - lo) * inv + 1.5 * 2^23, each operation rounded: the sum's low bits are the product
+  // rounded to nearest even, at most 15 since step is within 2^-9 of (hi - lo) / 15.  Four sums
+  // times 1, 16, 256, 4096 add up to four nibbles: the bits above the codes start at bit 22.
+  const uint64_t nlo = f2_pack(-lo, -lo);
   uint32_t c[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float xe = __uint_as_float((e & 1) ? (w[e >> 1] & 0xffff0000u) : (w[e >> 1] << 16));
-    // 1.5 * 2^23 added: the sum's low bits are the product rounded to nearest even
-    const float q = __fadd_rn(fminf(__fmul_rn(__fsub_rn(xe, lo), inv), 15.f), 12582912.f);
-    c[e] = __float_as_uint(q) & 15u;
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t x2 = f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+    float q0, q1;
+    f2_unpack(f2_add(x2, nlo), q0, q1);
+    c[2 * e] = __float_as_uint(__fadd_rn(__fmul_rn(q0, inv), 12582912.f));  // packed, the two would become one fma
+    c[2 * e + 1] = __float_as_uint(__fadd_rn(__fmul_rn(q1, inv), 12582912.f));
   }
-  piece0 = c[0] | (c[1] << 4) | (c[2] << 8) | (c[3] << 12);
-  piece1 = c[4] | (c[5] << 4) | (c[6] << 8) | (c[7] << 12);
+  piece0 = c[0] + c[1] * 16u + c[2] * 256u + c[3] * 4096u;  // only the low 16 bits count
+  piece1 = c[4] + c[5] * 16u + c[6] * 256u + c[7] * 4096u;
   param = static_cast<uint32_t>(__bfloat16_as_ushort(step16)) | (__float_as_uint(lo) & 0xffff0000u);
 }
 
@@ -72,7 +78,7 @@ __device__ __forceinline__ void store_row(uint32_t piece0, uint32_t piece1, uint
   // the odd one quarter 2 t + 1.
   const bool odd = j & 1;
   const uint32_t other = __shfl_xor_sync(kFull, odd ? piece0 : piece1, 4);
-  const uint32_t word = odd ? (other | (piece1 << 16)) : (piece0 | (other << 16));
+  const uint32_t word = odd ? __byte_perm(other, piece1, 0x5410) : __byte_perm(piece0, other, 0x5410);
   const int at = (2 * t + (odd ? 1 : 0)) * (2 * NG) + (j >> 1) * 4;
   if (dst != nullptr) {
     *reinterpret_cast<uint32_t*>(dst + at) = word;
@@ -84,42 +90,55 @@ __device__ __forceinline__ void store_row(uint32_t piece0, uint32_t piece1, uint
   }
 }
 
-// d/8 lanes a row; rows in the order (b, kept position, head), so that the reads are
-// consecutive.  blockIdx.y: 0 for k, 1 for v.
+// d/8 lanes a row; rows of a sequence in the order (kept position, head), so that the
+// reads are consecutive; two rows a thread in flight.  blockIdx.y: 0 for k, 1 for v;
+// blockIdx.z: the sequence.
+constexpr int kFillRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256)
     swa_kv4_fill_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, int P, uint8_t* kc, uint8_t* vc,
-                        uint8_t* sk, uint8_t* sv, int B, int Hkv, int W, int S) {
+                        uint8_t* sk, uint8_t* sv, int B, FastDiv hkv, int W, int S) {
   constexpr int LPR = D / 8;  // lanes a row
+  constexpr int PER = 256 / LPR;
   constexpr int ROW = kv4_row_bytes(D);
-  const uint4* src = blockIdx.y ? v : k;
-  uint8_t* ring = blockIdx.y ? vc : kc;
-  uint8_t* sink = blockIdx.y ? sv : sk;
+  const int Hkv = static_cast<int>(hkv.d);
   const int n_ring = min(P, W), first = P - n_ring;
   const int n_old = min(min(P, S), first);  // sinks that have left the window
-  const long long per_b = static_cast<long long>(n_ring + n_old) * Hkv;
-  const long long rows = per_b * B;
+  const int rows = (n_ring + n_old) * Hkv;
+  const int slot0 = first % W;              // ring slot of position `first`
   const int rl = threadIdx.x % LPR;
-  const long long stride = static_cast<long long>(gridDim.x) * (256 / LPR);
-  // every lane of a warp takes part in each step's shuffles
-  for (long long r0 = static_cast<long long>(blockIdx.x) * (256 / LPR); r0 < rows; r0 += stride) {
-    const long long r = r0 + threadIdx.x / LPR;
-    const bool real = r < rows;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    uint8_t *dst = nullptr, *dst2 = nullptr;
-    if (real) {
-      const int b = static_cast<int>(r / per_b);
-      const int in_b = static_cast<int>(r - b * per_b);
-      const int i = in_b / Hkv, h = in_b - i * Hkv;
-      const int p = i < n_old ? i : first + i - n_old;
-      x = src[((static_cast<size_t>(b) * P + p) * Hkv + h) * LPR + rl];
-      const size_t seg = static_cast<size_t>(b) * Hkv + h;
-      if (p >= first) dst = ring + (seg * W + p % W) * ROW;
-      if (p < S) dst2 = sink + (seg * S + p) * ROW;
+  for (int b = blockIdx.z; b < B; b += gridDim.z) {
+    const uint4* src = (blockIdx.y ? v : k) + static_cast<size_t>(b) * P * Hkv * LPR + rl;
+    uint8_t* ring = (blockIdx.y ? vc : kc) + static_cast<size_t>(b) * Hkv * W * ROW;
+    uint8_t* sink = (blockIdx.y ? sv : sk) + static_cast<size_t>(b) * Hkv * S * ROW;
+    // every lane of a warp takes part in each step's shuffles
+    for (int r0 = blockIdx.x * (PER * kFillRows); r0 < rows; r0 += gridDim.x * (PER * kFillRows)) {
+      uint4 x[kFillRows];
+      uint8_t *dst[kFillRows], *dst2[kFillRows];
+#pragma unroll
+      for (int u = 0; u < kFillRows; ++u) {
+        const int r = r0 + u * PER + threadIdx.x / LPR;
+        x[u] = make_uint4(0, 0, 0, 0);
+        dst[u] = dst2[u] = nullptr;
+        if (r < rows) {
+          const int i = static_cast<int>(hkv.div(r)), h = r - i * Hkv;
+          const int at = i - n_old;  // from the first kept ring position; negative: an old sink
+          const int p = at < 0 ? i : first + at;
+          x[u] = src[(static_cast<size_t>(p) * Hkv + h) * LPR];
+          if (at >= 0) {
+            const int slot = slot0 + at < W ? slot0 + at : slot0 + at - W;
+            dst[u] = ring + (static_cast<size_t>(h) * W + slot) * ROW;
+          }
+          if (p < S) dst2[u] = sink + (static_cast<size_t>(h) * S + p) * ROW;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFillRows; ++u) {
+        uint32_t p0, p1, param;
+        quantise8(x[u], p0, p1, param);
+        store_row<D>(p0, p1, param, rl, dst[u], dst2[u]);
+      }
     }
-    uint32_t p0, p1, param;
-    quantise8(x, p0, p1, param);
-    store_row<D>(p0, p1, param, rl, dst, dst2);
   }
 }
 
@@ -147,31 +166,32 @@ __global__ void __launch_bounds__(128)
 }
 
 // One lane per eight elements (group j, elements 8 t .. 8 t + 7: quarters 2 t, 2 t + 1).
+// blockIdx.y: 0 for k, 1 for v; blockIdx.z: the sequence.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256)
     swa_kv4_read_kernel(const int32_t* __restrict__ positions, int n, const uint8_t* __restrict__ kc,
                         const uint8_t* __restrict__ vc, const uint8_t* __restrict__ sk,
-                        const uint8_t* __restrict__ sv, void* k_out, void* v_out, int B, int Hkv, int W, int S) {
+                        const uint8_t* __restrict__ sv, void* k_out, void* v_out, int B, FastDiv hkv, FastDiv w, int S) {
   constexpr int LPR = D / 8, NG = D / kKv4Group;
   constexpr int ROW = kv4_row_bytes(D);
-  const uint8_t* ring = blockIdx.y ? vc : kc;
-  const uint8_t* sink = blockIdx.y ? sv : sk;
+  const int Hkv = static_cast<int>(hkv.d), W = static_cast<int>(w.d);
   void* out = blockIdx.y ? v_out : k_out;
-  const long long rows = static_cast<long long>(B) * n * Hkv;
+  const int rows = n * Hkv;
   const int rl = threadIdx.x % LPR, j = rl >> 2, t = rl & 3;
-  const long long stride = static_cast<long long>(gridDim.x) * (256 / LPR);
-  for (long long r = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / LPR; r < rows; r += stride) {
-    const long long bi = r / Hkv;
-    const int h = static_cast<int>(r - bi * Hkv);
-    const int b = static_cast<int>(bi / n);
-    const int p = positions[bi];
+  for (int b = blockIdx.z; b < B; b += gridDim.z)
+   for (int in_b = (blockIdx.x * 256 + threadIdx.x) / LPR; in_b < rows; in_b += gridDim.x * (256 / LPR)) {
+    const int i = static_cast<int>(hkv.div(in_b)), h = in_b - i * Hkv;
+    const int p = positions[static_cast<size_t>(b) * n + i];
+    const uint8_t* ring = blockIdx.y ? vc : kc;
+    const uint8_t* sink = blockIdx.y ? sv : sk;
+    const size_t r = static_cast<size_t>(b) * rows + in_b;
     float y[8];
     if (p < 0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = 0.f;
     } else {
       const size_t seg = static_cast<size_t>(b) * Hkv + h;
-      const uint8_t* row = p < S ? sink + (seg * S + p) * ROW : ring + (seg * W + p % W) * ROW;
+      const uint8_t* row = p < S ? sink + (seg * S + p) * ROW : ring + (seg * W + w.mod(p)) * ROW;
       const uint32_t c0 = *reinterpret_cast<const uint16_t*>(row + (2 * t) * 2 * NG + 2 * j);
       const uint32_t c1 = *reinterpret_cast<const uint16_t*>(row + (2 * t + 1) * 2 * NG + 2 * j);
       const uint32_t param = *reinterpret_cast<const uint32_t*>(row + D / 2 + 4 * j);
@@ -196,13 +216,22 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
+namespace {
+// Blocks along x for `units` blocks' worth of work of each of B sequences, k and v.
+dim3 kv4_grid(long long units, int B, int sms) {
+  const int z = std::min(B, 32768);
+  const long long x = std::min(units, std::max(1LL, sms * 64LL / (2LL * z)));
+  return dim3(static_cast<unsigned>(x), 2, static_cast<unsigned>(z));
+}
+}  // namespace
+
 cudaError_t launch_kv4_fill(const void* k, const void* v, int P, void* kc, void* vc, void* sk, void* sv, int B,
                             int Hkv, int d, int W, int S, int sms, cudaStream_t stream) {
   const int n_ring = std::min(P, W);
-  const long long rows = static_cast<long long>(B) * Hkv * (n_ring + std::min(std::min(P, S), P - n_ring));
-  if (rows == 0) return cudaSuccess;
-  const int per = 256 / (d / 8);
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((rows + per - 1) / per, sms * 16LL)), 2);
+  const long long rows = static_cast<long long>(Hkv) * (n_ring + std::min(std::min(P, S), P - n_ring));
+  const int per = 256 / (d / 8) * kFillRows;
+  const dim3 grid = kv4_grid((rows + per - 1) / per, B, sms);
+  const FastDiv hkv(Hkv);
   const auto* ks = static_cast<const uint4*>(k);
   const auto* vs = static_cast<const uint4*>(v);
   auto* c0 = static_cast<uint8_t*>(kc);
@@ -210,9 +239,9 @@ cudaError_t launch_kv4_fill(const void* k, const void* v, int P, void* kc, void*
   auto* s0 = static_cast<uint8_t*>(sk);
   auto* s1 = static_cast<uint8_t*>(sv);
   if (d == 128)
-    swa_kv4_fill_kernel<128><<<grid, 256, 0, stream>>>(ks, vs, P, c0, c1, s0, s1, B, Hkv, W, S);
+    swa_kv4_fill_kernel<128><<<grid, 256, 0, stream>>>(ks, vs, P, c0, c1, s0, s1, B, hkv, W, S);
   else
-    swa_kv4_fill_kernel<64><<<grid, 256, 0, stream>>>(ks, vs, P, c0, c1, s0, s1, B, Hkv, W, S);
+    swa_kv4_fill_kernel<64><<<grid, 256, 0, stream>>>(ks, vs, P, c0, c1, s0, s1, B, hkv, W, S);
   return cudaGetLastError();
 }
 
@@ -238,22 +267,21 @@ cudaError_t launch_kv4_append(const void* k, const void* v, const int32_t* pos, 
 cudaError_t launch_kv4_read(const int32_t* positions, int n, const void* kc, const void* vc, const void* sk,
                             const void* sv, void* k_out, void* v_out, bool f32, int B, int Hkv, int d, int W, int S,
                             int sms, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(B) * n * Hkv;
-  if (rows == 0) return cudaSuccess;
   const int per = 256 / (d / 8);
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((rows + per - 1) / per, sms * 32LL)), 2);
+  const dim3 grid = kv4_grid((static_cast<long long>(n) * Hkv + per - 1) / per, B, sms);
+  const FastDiv hkv(Hkv), w(W);
   const auto* c0 = static_cast<const uint8_t*>(kc);
   const auto* c1 = static_cast<const uint8_t*>(vc);
   const auto* s0 = static_cast<const uint8_t*>(sk);
   const auto* s1 = static_cast<const uint8_t*>(sv);
   if (d == 128 && f32)
-    swa_kv4_read_kernel<128, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, Hkv, W, S);
+    swa_kv4_read_kernel<128, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
   else if (d == 128)
-    swa_kv4_read_kernel<128, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, Hkv, W, S);
+    swa_kv4_read_kernel<128, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
   else if (f32)
-    swa_kv4_read_kernel<64, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, Hkv, W, S);
+    swa_kv4_read_kernel<64, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
   else
-    swa_kv4_read_kernel<64, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, Hkv, W, S);
+    swa_kv4_read_kernel<64, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
   return cudaGetLastError();
 }
 
