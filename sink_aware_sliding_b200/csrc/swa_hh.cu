@@ -77,13 +77,34 @@ __global__ void __launch_bounds__(kAppendThreads)
 // bits, histograms in shared memory): afterwards `cut` is the smallest kept key and
 // `ties` how many positions with exactly that key are kept, the earlier ones first.
 // Each warp then walks one contiguous stretch of positions, so that the kept ones come
-// out in ascending order after a prefix over the warps.
+// out in ascending order after a prefix over the warps.  The keys are read from global
+// memory once, all loads in flight, and stay in shared memory for the five walks over
+// them (four prompts of 16384, 8 heads: 28 us with every walk in global memory); prompts
+// longer than that go by global memory, four loads a thread in flight.
 constexpr int kFillThreads = 1024;
 constexpr int kFillWarps = kFillThreads / 32;
+constexpr int kFillKeys = 49152;  // keys in shared memory (192 KB)
+
+// Sum of `mine` over the threads before this one (all threads take part).
+__device__ __forceinline__ unsigned block_prefix(unsigned mine, unsigned* s_warp, int lane, int warp) {
+  unsigned incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  return __reduce_add_sync(kFull, lane < warp ? s_warp[lane] : 0u) + incl - mine;
+}
+
+template <bool SMEM>
 __global__ void __launch_bounds__(kFillThreads)
     swa_hh_select_kernel(const float* __restrict__ score_in, int L, int32_t* slot_pos, float* score, int C, int S,
                          int recent) {
+  extern __shared__ uint32_t s_keys[];
   __shared__ unsigned s_hist[2048];
+  __shared__ unsigned s_warp[kFillWarps];
   __shared__ unsigned s_cut, s_left;
   __shared__ int s_kept[kFillWarps], s_ties[kFillWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -97,6 +118,15 @@ __global__ void __launch_bounds__(kFillThreads)
     }
     return;
   }
+  if constexpr (SMEM) {
+#pragma unroll 8
+    for (int i = tid; i < L; i += kFillThreads) s_keys[i] = order_bits(in[i]);
+    __syncthreads();
+  }
+  auto key_at = [&](int i) -> uint32_t {
+    if constexpr (SMEM) return s_keys[i];
+    return order_bits(in[i]);
+  };
   const int lo = S, hi = L - recent;          // positions that compete
   unsigned prefix = 0, need = C - S - recent;  // need <= hi - lo, as L > C
   // need = 0: nothing competes successfully; cut above every key
@@ -110,34 +140,25 @@ __global__ void __launch_bounds__(kFillThreads)
       const unsigned bins = 1u << kBits[pass];
       for (unsigned i = tid; i < bins; i += kFillThreads) s_hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = lo + tid; i < hi; i += kFillThreads) {
-        const uint32_t key = order_bits(in[i]);
+        const uint32_t key = key_at(i);
         if (pass == 0 || (key >> (shift + kBits[pass])) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
       }
       __syncthreads();
-      if (warp == 0) {
-        // from the top: lane 0 has the largest bins
-        const unsigned per = bins / 32;
-        unsigned sum = 0;
-        for (unsigned i = 0; i < per; ++i) sum += s_hist[bins - 1 - (lane * per + i)];
-        unsigned incl = sum;
+      // from the top bin down, one or two neighbouring bins a thread
+      constexpr unsigned kPer[3] = {2, 2, 1};
+      unsigned n[2] = {0, 0};
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned y = __shfl_up_sync(kFull, incl, o);
-          if (lane >= o) incl += y;
+      for (unsigned i = 0; i < kPer[pass]; ++i) n[i] = s_hist[bins - 1 - (tid * kPer[pass] + i)];
+      unsigned above = block_prefix(n[0] + n[1], s_warp, lane, warp);
+#pragma unroll
+      for (unsigned i = 0; i < kPer[pass]; ++i) {
+        if (above < need && above + n[i] >= need) {  // one bin of one thread
+          s_cut = (prefix << kBits[pass]) | (bins - 1 - (tid * kPer[pass] + i));
+          s_left = need - above;
         }
-        unsigned above = incl - sum;
-        if (above < need && need <= incl) {  // one lane
-          for (unsigned i = 0; i < per; ++i) {
-            const unsigned bin = bins - 1 - (lane * per + i);
-            if (above + s_hist[bin] >= need) {
-              s_cut = (prefix << kBits[pass]) | bin;
-              s_left = need - above;
-              break;
-            }
-            above += s_hist[bin];
-          }
-        }
+        above += n[i];
       }
       __syncthreads();
       prefix = s_cut;
@@ -150,47 +171,48 @@ __global__ void __launch_bounds__(kFillThreads)
   // ---- compaction: stretch of this warp
   const int per = ((L + kFillWarps - 1) / kFillWarps + 31) / 32 * 32;
   const int first = min(L, warp * per), last = min(L, first + per);
-  int n_kept = 0, n_ties = 0;
-  for (int i0 = first; i0 < last; i0 += 32) {
-    const int i = i0 + lane;
-    bool above = false, equal = false;
+  auto kind = [&](int i, bool& above, bool& equal) {
+    above = equal = false;
     if (i < last) {
       const bool always = i < lo || i >= hi;
-      const uint32_t key = always ? 0u : order_bits(in[i]);
+      const uint32_t key = key_at(i);
       above = always || (ties > 0 && key > cut);
       equal = !always && ties > 0 && key == cut;
     }
-    n_kept += __popc(__ballot_sync(kFull, above));
-    n_ties += __popc(__ballot_sync(kFull, equal));
+  };
+  int n_kept = 0, n_ties = 0;
+#pragma unroll 4
+  for (int i0 = first; i0 < last; i0 += 32) {
+    bool above, equal;
+    kind(i0 + lane, above, equal);
+    n_kept += above;
+    n_ties += equal;
   }
+  n_kept = __reduce_add_sync(kFull, n_kept);
+  n_ties = __reduce_add_sync(kFull, n_ties);
   if (lane == 0) {
     s_kept[warp] = n_kept;
     s_ties[warp] = n_ties;
   }
   __syncthreads();
-  int out = 0, tie = 0;  // kept without ties, and ties, in the stretches before
-  for (int w = 0; w < warp; ++w) {
-    out += s_kept[w];
-    tie += s_ties[w];
-  }
+  // kept without ties, and ties, in the stretches before
+  int out = __reduce_add_sync(kFull, lane < warp ? s_kept[lane] : 0);
+  int tie = __reduce_add_sync(kFull, lane < warp ? s_ties[lane] : 0);
+#pragma unroll 4
   for (int i0 = first; i0 < last; i0 += 32) {
     const int i = i0 + lane;
-    bool above = false, equal = false;
-    float x = 0.f;
-    if (i < last) {
-      x = in[i];
-      const bool always = i < lo || i >= hi;
-      const uint32_t key = always ? 0u : order_bits(x);
-      above = always || (ties > 0 && key > cut);
-      equal = !always && ties > 0 && key == cut;
-    }
+    bool above, equal;
+    kind(i, above, equal);
     const unsigned ma = __ballot_sync(kFull, above), me = __ballot_sync(kFull, equal);
     const unsigned below = (1u << lane) - 1;
     const int my_tie = tie + __popc(me & below);
     const int slot = out + __popc(ma & below) + min(my_tie, static_cast<int>(ties));
     if (above || (equal && my_tie < static_cast<int>(ties))) {
       sp[slot] = i;
-      sc[slot] = x;
+      // the key gives the score back, but for NaN and the zeros' signs
+      const uint32_t key = key_at(i);
+      sc[slot] = !SMEM || key == 0u || key == 0x80000000u ? in[i]
+                 : __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
     }
     out += __popc(ma);
     tie += __popc(me);
@@ -230,8 +252,16 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
                            int32_t* slot_pos, float* score, int B, int Hkv, int d, int C, int S, int recent, int sms,
                            cudaStream_t stream) {
   const int segs = B * Hkv;
-  swa_hh_select_kernel<<<segs, kFillThreads, 0, stream>>>(score_in, L, slot_pos, score, C, S, recent);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (L <= kFillKeys) {
+    const size_t smem = L > C ? static_cast<size_t>(L) * 4 : 0;
+    e = cudaFuncSetAttribute(swa_hh_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFillKeys * 4);
+    if (e != cudaSuccess) return e;
+    swa_hh_select_kernel<true><<<segs, kFillThreads, smem, stream>>>(score_in, L, slot_pos, score, C, S, recent);
+  } else {
+    swa_hh_select_kernel<false><<<segs, kFillThreads, 0, stream>>>(score_in, L, slot_pos, score, C, S, recent);
+  }
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int kept = std::min(L, C);
   if (kept == 0) return cudaSuccess;

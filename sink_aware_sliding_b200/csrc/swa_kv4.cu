@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(256)
   const int rows = n * Hkv;
   const int rl = threadIdx.x % LPR, j = rl >> 2, t = rl & 3;
   for (int b = blockIdx.z; b < B; b += gridDim.z)
-   for (int in_b = (blockIdx.x * 256 + threadIdx.x) / LPR; in_b < rows; in_b += gridDim.x * (256 / LPR)) {
+#pragma unroll 2
+    for (int in_b = (blockIdx.x * 256 + threadIdx.x) / LPR; in_b < rows; in_b += gridDim.x * (256 / LPR)) {
     const int i = static_cast<int>(hkv.div(in_b)), h = in_b - i * Hkv;
     const int p = positions[static_cast<size_t>(b) * n + i];
     const uint8_t* ring = blockIdx.y ? vc : kc;
@@ -197,8 +198,15 @@ __global__ void __launch_bounds__(256)
       const uint32_t param = *reinterpret_cast<const uint32_t*>(row + D / 2 + 4 * j);
       const float step = __uint_as_float(param << 16), lo = __uint_as_float(param & 0xffff0000u);
       const uint32_t c = c0 | (c1 << 16);
+      // nibbles to bytes, each byte to the low mantissa bits of 2^23, and off again
+      const uint32_t even = c & 0x0f0f0f0fu, odd = (c >> 4) & 0x0f0f0f0fu;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(static_cast<float>((c >> (4 * e)) & 15u), step, lo);
+      for (int e = 0; e < 4; ++e) {
+        const float n0 = __uint_as_float(__byte_perm(even, 0x4b000000u, 0x7440 + e)) - 8388608.f;
+        const float n1 = __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7440 + e)) - 8388608.f;
+        y[2 * e] = fmaf(n0, step, lo);
+        y[2 * e + 1] = fmaf(n1, step, lo);
+      }
     }
     if constexpr (F32) {
       float4* o = static_cast<float4*>(out) + (r * LPR + rl) * 2;
@@ -217,10 +225,11 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 namespace {
-// Blocks along x for `units` blocks' worth of work of each of B sequences, k and v.
-dim3 kv4_grid(long long units, int B, int sms) {
+// Blocks along x for `units` blocks' worth of work of each of B sequences, k and v: as many
+// as an SM holds at once (`per_sm`), since a block's start costs as much as two of its rows.
+dim3 kv4_grid(long long units, int B, int sms, int per_sm) {
   const int z = std::min(B, 32768);
-  const long long x = std::min(units, std::max(1LL, sms * 64LL / (2LL * z)));
+  const long long x = std::min(units, std::max(1LL, static_cast<long long>(sms) * per_sm / (2LL * z)));
   return dim3(static_cast<unsigned>(x), 2, static_cast<unsigned>(z));
 }
 }  // namespace
@@ -230,7 +239,7 @@ cudaError_t launch_kv4_fill(const void* k, const void* v, int P, void* kc, void*
   const int n_ring = std::min(P, W);
   const long long rows = static_cast<long long>(Hkv) * (n_ring + std::min(std::min(P, S), P - n_ring));
   const int per = 256 / (d / 8) * kFillRows;
-  const dim3 grid = kv4_grid((rows + per - 1) / per, B, sms);
+  const dim3 grid = kv4_grid((rows + per - 1) / per, B, sms, 16);
   const FastDiv hkv(Hkv);
   const auto* ks = static_cast<const uint4*>(k);
   const auto* vs = static_cast<const uint4*>(v);
@@ -268,7 +277,7 @@ cudaError_t launch_kv4_read(const int32_t* positions, int n, const void* kc, con
                             const void* sv, void* k_out, void* v_out, bool f32, int B, int Hkv, int d, int W, int S,
                             int sms, cudaStream_t stream) {
   const int per = 256 / (d / 8);
-  const dim3 grid = kv4_grid((static_cast<long long>(n) * Hkv + per - 1) / per, B, sms);
+  const dim3 grid = kv4_grid((static_cast<long long>(n) * Hkv + per - 1) / per, B, sms, 16);
   const FastDiv hkv(Hkv), w(W);
   const auto* c0 = static_cast<const uint8_t*>(kc);
   const auto* c1 = static_cast<const uint8_t*>(vc);

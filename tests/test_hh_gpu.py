@@ -99,6 +99,20 @@ def test_fill_keeps_what_the_oracle_keeps(d, L, C, S, recent, kind):
             assert (kc[b, h, n:] == 5).all() and (vc[b, h, n:] == 5).all()
 
 
+def test_fill_of_a_prompt_whose_keys_do_not_fit_shared_memory():
+    B, H, d, L, C, S, recent = 1, 2, 64, 60001, 1000, 4, 100
+    k = rand((B, L, H, d), 1)
+    s = np.floor(np.random.default_rng(3).random((B, H, L)) * 400).astype(np.float32)  # many ties
+    kc, vc = (torch.zeros(B, H, C, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sp, score = torch.zeros(B, H, C, device="cuda", dtype=torch.int32), torch.zeros(B, H, C, device="cuda")
+    swa.swa_hh_cache_fill(k.cuda(), (-k).cuda(), torch.from_numpy(s).cuda(), kc, vc, sp, score, S, recent)
+    torch.cuda.synchronize()
+    for h in range(H):
+        keep = oracle.hh_select(s[0, h], C, S, recent)
+        assert sp[0, h].cpu().tolist() == keep
+        assert torch.equal(kc[0, h].cpu(), k[0, keep, h]) and torch.equal(vc[0, h].cpu(), -k[0, keep, h])
+
+
 # ---------------------------------------------------------------- appending
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("C,S,recent", [(1, 0, 1), (4, 1, 3), (5, 0, 1), (300, 4, 64), (700, 0, 512)])
