@@ -390,53 +390,54 @@ def swa_kv4_row_bytes(d: int) -> int:
     return int(_load().swa_kv4_row_bytes(int(d)))
 
 
-class _Args:
-    """Addresses of one call's tensors, each checked: contiguous, on the current device, of the type and shape
-    named.  The checks read as little as they can and put no text together unless they fail: a decode step's
-    launches take a few microseconds, and so should what comes before them."""
+# A decode step's launches take a few microseconds, and so should what comes before them: the checks of the
+# functions below read as little as they can and put no text together unless they fail.
+_torch = None
 
-    __slots__ = ("dev",)
 
-    def __init__(self, t, name: str):
+def _device(t, name: str) -> int:
+    """The current CUDA device, which t has to be on."""
+    global _torch
+    if _torch is None:
         import torch
-        if not t.is_cuda:
-            raise ValueError(f"{name}: CUDA tensor")
-        self.dev = torch.cuda.current_device()
-
-    def __call__(self, t, name: str, dtype, shape) -> int:
-        if t.dtype is not dtype or t.get_device() != self.dev or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on the current CUDA device")
-        return t.data_ptr()
-
-    def stream(self, stream):
-        if stream is not None:
-            return _stream(stream)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self.dev)
+        _torch = torch
+    dev = t.get_device()
+    if dev < 0 or dev != _torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on the current CUDA device")
+    return dev
 
 
-def _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
-    import torch
-    u8 = torch.uint8
+def _at(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on the current CUDA device")
+    return t.data_ptr()
+
+
+def _on(stream, dev: int):
+    return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
+    u8 = _torch.uint8
     row = d // 2 + d // 8
     ring = (B, Hkv, window, row)
     if n_sink <= 0:
-        return at(kcache, "kcache", u8, ring), at(vcache, "vcache", u8, ring), None, None
+        return _at(kcache, "kcache", u8, ring, dev), _at(vcache, "vcache", u8, ring, dev), None, None
     sink = (B, Hkv, n_sink, row)
-    return (at(kcache, "kcache", u8, ring), at(vcache, "vcache", u8, ring), at(sink_k, "sink_k", u8, sink),
-            at(sink_v, "sink_v", u8, sink))
+    return (_at(kcache, "kcache", u8, ring, dev), _at(vcache, "vcache", u8, ring, dev),
+            _at(sink_k, "sink_k", u8, sink, dev), _at(sink_v, "sink_v", u8, sink, dev))
 
 
 def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink: int, stream=None) -> None:
     """Quantise prefix positions 0..P-1 of k/v [B, P, Hkv, d] (bf16) into an empty 4-bit ring cache:
     kcache/vcache [B, Hkv, window, row] uint8, sink_k/sink_v [B, Hkv, n_sink, row] (None without sinks)."""
-    import torch
     _need(k.dim() == 4, "k [B, P, Hkv, d]")
-    at = _Args(k, "k")
+    dev = _device(k, "k")
     B, P, Hkv, d = shape = k.shape
-    kp, vp = at(k, "k", torch.bfloat16, shape), at(v, "v", torch.bfloat16, shape)
-    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, at.stream(stream))
+    kp, vp = _at(k, "k", _torch.bfloat16, shape, dev), _at(v, "v", _torch.bfloat16, shape, dev)
+    cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_fill")
 
@@ -444,14 +445,13 @@ def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink
 def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, window: int, n_sink: int,
                          stream=None) -> None:
     """Quantise k_new/v_new [B, Hkv, d] (bf16) of positions pos (int32 [B]) into the 4-bit ring cache."""
-    import torch
     _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
-    at = _Args(k_new, "k_new")
+    dev = _device(k_new, "k_new")
     B, Hkv, d = shape = k_new.shape
-    kp, vp = at(k_new, "k_new", torch.bfloat16, shape), at(v_new, "v_new", torch.bfloat16, shape)
-    pp = at(pos, "pos", torch.int32, (B,))
-    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, at.stream(stream))
+    kp, vp = _at(k_new, "k_new", _torch.bfloat16, shape, dev), _at(v_new, "v_new", _torch.bfloat16, shape, dev)
+    pp = _at(pos, "pos", _torch.int32, (B,), dev)
+    cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_append")
 
@@ -459,42 +459,44 @@ def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, wind
 def swa_kv4_cache_read(positions, kcache, vcache, sink_k, sink_v, k_out, v_out, window: int, n_sink: int,
                        stream=None) -> None:
     """The values of cached positions (int32 [B, n]) into k_out/v_out [B, n, Hkv, d] (both bf16 or both float32)."""
-    import torch
-    _need(k_out.dim() == 4 and k_out.dtype in (torch.bfloat16, torch.float32), "k_out [B, n, Hkv, d] bf16 or float32")
-    at = _Args(k_out, "k_out")
+    dev = _device(k_out, "k_out")
+    _need(k_out.dim() == 4 and k_out.dtype in (_torch.bfloat16, _torch.float32), "k_out [B, n, Hkv, d] bf16 or float32")
     B, n, Hkv, d = shape = k_out.shape
-    ko, vo = at(k_out, "k_out", k_out.dtype, shape), at(v_out, "v_out", k_out.dtype, shape)
-    pp = at(positions, "positions", torch.int32, (B, n))
-    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    code = SWA_DTYPE_F32 if k_out.dtype is torch.float32 else SWA_DTYPE_BF16
-    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, at.stream(stream))
+    ko, vo = _at(k_out, "k_out", k_out.dtype, shape, dev), _at(v_out, "v_out", k_out.dtype, shape, dev)
+    pp = _at(positions, "positions", _torch.int32, (B, n), dev)
+    cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    code = SWA_DTYPE_F32 if k_out.dtype is _torch.float32 else SWA_DTYPE_BF16
+    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_read")
 
 
 def _decode_io(q, out, lse):
-    import torch
-    code = {torch.bfloat16: SWA_DTYPE_BF16, torch.float32: SWA_DTYPE_BF16_F32OUT}.get(out.dtype)
-    _need(q.dim() == 3 and code is not None, "q [B, Hq, d], out bf16 or float32")
-    at = _Args(q, "q")
-    shape = q.shape
-    return (at, at(q, "q", torch.bfloat16, shape), at(out, "out", out.dtype, shape),
-            None if lse is None else at(lse, "lse", torch.float32, shape[:2]), code)
+    dev = _device(q, "q")
+    dtype, shape = out.dtype, q.shape
+    if dtype is _torch.bfloat16:
+        code = SWA_DTYPE_BF16
+    elif dtype is _torch.float32:
+        code = SWA_DTYPE_BF16_F32OUT
+    else:
+        raise ValueError("out bf16 or float32")
+    _need(len(shape) == 3, "q [B, Hq, d]")
+    return (dev, _at(q, "q", _torch.bfloat16, shape, dev), _at(out, "out", dtype, shape, dev),
+            None if lse is None else _at(lse, "lse", _torch.float32, shape[:2], dev), code)
 
 
 def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int, n_sink: int, scale=None,
                    stream=None) -> None:
     """One decode step over the 4-bit ring cache; q [B, Hq, d] bf16 at positions pos (int32 [B]);
     writes out [B, Hq, d] (bf16 or float32) and lse [B, Hq] (or None).  No workspace."""
-    import torch
-    at, qp, op, lp, code = _decode_io(q, out, lse)
+    dev, qp, op, lp, code = _decode_io(q, out, lse)
     B, Hq, d = q.shape
     _need(kcache.dim() == 4, "kcache [B, Hkv, window, row]")
     Hkv = kcache.shape[1]
-    pp = at(pos, "pos", torch.int32, (B,))
-    cache = _kv4_cache(at, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
+    pp = _at(pos, "pos", _torch.int32, (B,), dev)
+    cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
     st = _load().swa_kv4_decode(qp, *cache, pp, op, lp, B, Hq, Hkv, d, window, n_sink, _scale(scale, d), code,
-                                at.stream(stream))
+                                _on(stream, dev))
     if st:
         _check(st, "swa_kv4_decode")
 
@@ -502,39 +504,36 @@ def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int
 def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=None, stream=None) -> None:
     """Attention weight each key of a prompt received from the last n_obs queries: q [B, L, Hq, d],
     k [B, L, Hkv, d] bf16 and lse [B, Hq, L] as swa_fwd takes and leaves them; writes score [B, Hkv, L] float32."""
-    import torch
     _need(q.dim() == 4 and k.dim() == 4, "q [B, L, Hq, d], k [B, L, Hkv, d]")
-    at = _Args(q, "q")
+    dev = _device(q, "q")
     B, L, Hq, d = q.shape
     Hkv = k.shape[2]
-    st = _load().swa_hh_scores(at(q, "q", torch.bfloat16, q.shape), at(k, "k", torch.bfloat16, (B, L, Hkv, d)),
-                               at(lse, "lse", torch.float32, (B, Hq, L)),
-                               at(score, "score", torch.float32, (B, Hkv, L)), B, Hq, Hkv, L, d, n_obs, window,
-                               n_sink, _scale(scale, d), at.stream(stream))
+    st = _load().swa_hh_scores(_at(q, "q", _torch.bfloat16, q.shape, dev), _at(k, "k", _torch.bfloat16, (B, L, Hkv, d), dev),
+                               _at(lse, "lse", _torch.float32, (B, Hq, L), dev),
+                               _at(score, "score", _torch.float32, (B, Hkv, L), dev), B, Hq, Hkv, L, d, n_obs, window,
+                               n_sink, _scale(scale, d), _on(stream, dev))
     if st:
         _check(st, "swa_hh_scores")
 
 
-def _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d):
-    import torch
+def _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d):
     _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
     C = kcache.shape[2]
     rows, slots = (B, Hkv, C, d), (B, Hkv, C)
-    return C, (at(kcache, "kcache", torch.bfloat16, rows), at(vcache, "vcache", torch.bfloat16, rows),
-               at(slot_pos, "slot_pos", torch.int32, slots), at(score, "score", torch.float32, slots))
+    return C, (_at(kcache, "kcache", _torch.bfloat16, rows, dev), _at(vcache, "vcache", _torch.bfloat16, rows, dev),
+               _at(slot_pos, "slot_pos", _torch.int32, slots, dev), _at(score, "score", _torch.float32, slots, dev))
 
 
 def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: int, recent: int, stream=None) -> None:
     """Keep the first n_sink, the last `recent` and the heaviest other positions of a prompt k/v
     [B, L, Hkv, d] (bf16), weights score_in [B, Hkv, L], in a cache of capacity kcache.shape[2]."""
-    import torch
     _need(k.dim() == 4, "k [B, L, Hkv, d]")
-    at = _Args(k, "k")
+    dev = _device(k, "k")
     B, L, Hkv, d = shape = k.shape
-    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_cache_fill(at(k, "k", torch.bfloat16, shape), at(v, "v", torch.bfloat16, shape),
-                                   at(score_in, "score_in", torch.float32, (B, Hkv, L)), L, *cache, B, Hkv, d, C,
-                                   n_sink, recent, at.stream(stream))
+    C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_fill(_at(k, "k", _torch.bfloat16, shape, dev), _at(v, "v", _torch.bfloat16, shape, dev),
+                                   _at(score_in, "score_in", _torch.float32, (B, Hkv, L), dev), L, *cache, B, Hkv, d, C,
+                                   n_sink, recent, _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_fill")
 
@@ -543,15 +542,14 @@ def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot
                         stream=None) -> None:
     """Write k_new/v_new [B, Hkv, d] (bf16) of positions pos (int32 [B]) into the slot of that position,
     an empty slot, or the lightest slot that may be evicted; slot int32 [B, Hkv] (or None) receives which."""
-    import torch
     _need(k_new.dim() == 3, "k_new [B, Hkv, d]")
-    at = _Args(k_new, "k_new")
+    dev = _device(k_new, "k_new")
     B, Hkv, d = shape = k_new.shape
-    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_cache_append(at(k_new, "k_new", torch.bfloat16, shape),
-                                     at(v_new, "v_new", torch.bfloat16, shape), at(pos, "pos", torch.int32, (B,)),
-                                     *cache, None if slot is None else at(slot, "slot", torch.int32, (B, Hkv)), B, Hkv,
-                                     d, C, n_sink, recent, at.stream(stream))
+    C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_cache_append(_at(k_new, "k_new", _torch.bfloat16, shape, dev),
+                                     _at(v_new, "v_new", _torch.bfloat16, shape, dev), _at(pos, "pos", _torch.int32, (B,), dev),
+                                     *cache, None if slot is None else _at(slot, "slot", _torch.int32, (B, Hkv), dev), B, Hkv,
+                                     d, C, n_sink, recent, _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_append")
 
@@ -559,12 +557,12 @@ def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot
 def swa_hh_decode(q, kcache, vcache, slot_pos, score, out, lse, scale=None, decay: float = 1.0, stream=None) -> None:
     """One decode step over the occupied slots; q [B, Hq, d] bf16; writes out [B, Hq, d] (bf16 or float32)
     and lse [B, Hq] (or None), and sets score = decay * score + the slot's softmax weights."""
-    at, qp, op, lp, code = _decode_io(q, out, lse)
+    dev, qp, op, lp, code = _decode_io(q, out, lse)
     B, Hq, d = q.shape
     _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
     Hkv = kcache.shape[1]
-    C, cache = _hh_cache(at, kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), decay, code, at.stream(stream))
+    C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
+    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), decay, code, _on(stream, dev))
     if st:
         _check(st, "swa_hh_decode")
 
@@ -585,23 +583,22 @@ def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_b
     """Rotate q [T, Hq, d] and k [T, Hkv, d] (k may be None; bf16 or float32) in place by positions of several
     axes (int32 [n_axes, T]); sections: pairs of each axis, their sum d/2; layout "sections", "per_axis" or
     "interleaved".  The tokens of q and k may be strided views.  inverse=True turns back (the backward pass)."""
-    import torch
-    _need(q.dim() == 3 and q.dtype in (torch.bfloat16, torch.float32), "q [T, Hq, d] bf16 or float32")
+    dev = _device(q, "q")
+    _need(q.dim() == 3 and q.dtype in (_torch.bfloat16, _torch.float32), "q [T, Hq, d] bf16 or float32")
     if layout not in _ROPE_LAYOUTS:
         raise ValueError(f"layout one of {sorted(_ROPE_LAYOUTS)}")
-    at = _Args(q, "q")
     T, _, d = q.shape
-    qp, Hq, qs = _rope_rows(q, "q", T, d, at.dev)
+    qp, Hq, qs = _rope_rows(q, "q", T, d, dev)
     kp, Hkv, ks = None, 0, 0
     if k is not None:
         _need(k.dtype is q.dtype, "k of q's type")
-        kp, Hkv, ks = _rope_rows(k, "k", T, d, at.dev)
+        kp, Hkv, ks = _rope_rows(k, "k", T, d, dev)
     n_axes = len(sections)
-    pp = at(positions, "positions", torch.int32, (n_axes, T))
+    pp = _at(positions, "positions", _torch.int32, (n_axes, T), dev)
     sec = (ctypes.c_int32 * max(1, n_axes))(*sections)
     st = _load().swa_rope_axes_qk(qp, kp, pp, T, Hq, Hkv, d, qs, ks, sec, n_axes, _ROPE_LAYOUTS[layout],
                                   rope_base, 1 if inverse else 0,
-                                  SWA_DTYPE_F32 if q.dtype is torch.float32 else SWA_DTYPE_BF16, at.stream(stream))
+                                  SWA_DTYPE_F32 if q.dtype is _torch.float32 else SWA_DTYPE_BF16, _on(stream, dev))
     if st:
         _check(st, "swa_rope_axes_qk")
 

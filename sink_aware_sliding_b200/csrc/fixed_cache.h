@@ -2,6 +2,7 @@
 // that evicts by accumulated attention weight, and rotary positions with axes.
 #pragma once
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace swa {
@@ -19,6 +20,21 @@ struct FastDiv {
   __device__ __forceinline__ uint32_t mod(uint32_t n) const { return n - div(n) * d; }
 #endif
 };
+
+// Let a kernel use up to `bytes` of dynamic shared memory: asked of the runtime once per
+// device, since the question costs as much as a tenth of a launch.
+template <auto Kernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // ---------------------------------------------------------------- 4-bit ring cache
 constexpr int kKv4Group = 32;  // elements that share a step and a minimum

@@ -255,7 +255,7 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
   cudaError_t e = cudaSuccess;
   if (L <= kFillKeys) {
     const size_t smem = L > C ? static_cast<size_t>(L) * 4 : 0;
-    e = cudaFuncSetAttribute(swa_hh_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFillKeys * 4);
+    e = allow_shared<swa_hh_select_kernel<true>>(kFillKeys * 4);
     if (e != cudaSuccess) return e;
     swa_hh_select_kernel<true><<<segs, kFillThreads, smem, stream>>>(score_in, L, slot_pos, score, C, S, recent);
   } else {

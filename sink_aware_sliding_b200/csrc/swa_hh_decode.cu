@@ -288,8 +288,7 @@ cudaError_t launch_impl(const HhDecodeArgs& a, int sms, cudaStream_t stream) {
   while (c < 8 && smem_of(c) > kTwo) c *= 2;
   const size_t smem = smem_of(c);
   if (smem > kMost || segments * c > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(swa_hh_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kMost));
+  cudaError_t e = allow_shared<swa_hh_decode_kernel<D>>(static_cast<int>(kMost));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
@@ -301,7 +300,7 @@ cudaError_t launch_impl(const HhDecodeArgs& a, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.x = static_cast<unsigned>(c);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = c > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, swa_hh_decode_kernel<D>, a, c);
 }
 

@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "fixed_cache.h"
 #include "hh_scores.h"
 #include "prefill_common.cuh"
 #include "ptx.cuh"
@@ -338,7 +339,7 @@ cudaError_t launch_impl(const HhScoresArgs& a, const CUtensorMap& tq, const CUte
                         cudaStream_t stream) {
   auto kern = swa_hh_scores_kernel<D>;
   static_assert(Cfg<D>::SMEM <= 232448, "shared memory budget");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  cudaError_t e = allow_shared<swa_hh_scores_kernel<D>>(Cfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, Cfg<D>::SMEM, stream>>>(a, tq, tk);
   return cudaGetLastError();

@@ -369,8 +369,7 @@ cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   const long long tiles = (static_cast<long long>(a.W) + a.S + kRows - 1) / kRows;
   const int c = decode_cluster(segments, tiles, sms, kBlocksPerSm, 1);
   if (segments * c > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(swa_kv4_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = allow_shared<swa_kv4_decode_kernel<D>>(static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
@@ -382,7 +381,7 @@ cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.x = static_cast<unsigned>(c);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = c > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, swa_kv4_decode_kernel<D>, a, c);
 }
 
