@@ -99,18 +99,21 @@ def test_fill_keeps_what_the_oracle_keeps(d, L, C, S, recent, kind):
             assert (kc[b, h, n:] == 5).all() and (vc[b, h, n:] == 5).all()
 
 
-def test_fill_of_a_prompt_whose_keys_do_not_fit_shared_memory():
-    B, H, d, L, C, S, recent = 1, 2, 64, 60001, 1000, 4, 100
+@pytest.mark.parametrize("B,H,L,C", [(1, 2, 60001, 1000), (1, 1, 500003, 3000), (40, 4, 50001, 700), (5, 4, 9000, 2500)])
+def test_fill_of_long_prompts(B, H, L, C):
+    """Prompts whose keys do not fit shared memory, and one whose do, with many ties."""
+    d, S, recent = 64, 4, 100
     k = rand((B, L, H, d), 1)
     s = np.floor(np.random.default_rng(3).random((B, H, L)) * 400).astype(np.float32)  # many ties
     kc, vc = (torch.zeros(B, H, C, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
     sp, score = torch.zeros(B, H, C, device="cuda", dtype=torch.int32), torch.zeros(B, H, C, device="cuda")
     swa.swa_hh_cache_fill(k.cuda(), (-k).cuda(), torch.from_numpy(s).cuda(), kc, vc, sp, score, S, recent)
     torch.cuda.synchronize()
-    for h in range(H):
-        keep = oracle.hh_select(s[0, h], C, S, recent)
-        assert sp[0, h].cpu().tolist() == keep
-        assert torch.equal(kc[0, h].cpu(), k[0, keep, h]) and torch.equal(vc[0, h].cpu(), -k[0, keep, h])
+    for b, h in {(0, 0), (B - 1, H - 1), (B // 2, 0)}:
+        keep = oracle.hh_select(s[b, h], C, S, recent)
+        assert sp[b, h].cpu().tolist() == keep
+        assert torch.equal(kc[b, h].cpu(), k[b, keep, h]) and torch.equal(vc[b, h].cpu(), -k[b, keep, h])
+        np.testing.assert_array_equal(score[b, h].cpu().numpy(), s[b, h, keep])
 
 
 # ---------------------------------------------------------------- appending
