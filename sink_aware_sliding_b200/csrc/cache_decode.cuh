@@ -186,6 +186,31 @@ __device__ __forceinline__ void merge_done(int c) {
   if (c > 1) cooperative_groups::this_cluster().barrier_wait();
 }
 
+// A decode kernel is launched while the kernel before it (the step's append, mostly) still
+// runs, and waits here for that kernel's end and its writes: the launch and the blocks'
+// start are out of the way by then.  The append kernels let it go at once.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launch with clusters of c blocks that may start early (see above).
+template <typename Kernel, typename Args>
+cudaError_t launch_decode_cluster(Kernel kernel, const Args& a, long long segments, int c, size_t smem,
+                                  cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
+  cfg.blockDim = dim3(kDecWarps * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, c);
+}
+
 // Blocks per cluster: enough that `segments` fill the GPU about `waves` times over,
 // but at least kDecWarps tiles for each block and at most 8 (the portable size).
 inline int decode_cluster(long long segments, long long tiles, int sms, int blocks_per_sm, int waves) {

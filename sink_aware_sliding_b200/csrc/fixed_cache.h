@@ -21,6 +21,12 @@ struct FastDiv {
 #endif
 };
 
+#ifdef __CUDACC__
+// In a kernel that a decode follows: the decode's blocks may start (they wait for this
+// kernel's end before they read anything).
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+#endif
+
 // Let a kernel use up to `bytes` of dynamic shared memory: asked of the runtime once per
 // device, since the question costs as much as a tenth of a launch.
 template <auto Kernel>

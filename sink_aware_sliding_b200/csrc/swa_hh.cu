@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kAppendThreads)
                          uint4* kc, uint4* vc, int32_t* slot_pos, float* score, int32_t* slot, int Hkv, int vec,
                          int C, int S, int recent) {
   __shared__ unsigned long long s_best[kAppendThreads / 32];
+  let_next_kernel_start();
   const size_t seg = blockIdx.x;
   const int p = pos[seg / Hkv];
   if (p < 0) {

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, 2) swa_hh_decode_kernel(const 
     cp_async_commit();
   };
 
+  wait_for_previous_kernel();
   int tile = rank * kDecWarps + warp;
   unsigned masks[kStages];  // of the tiles tile, tile + nw, ...
   int ahead;                // slots of the first tile that has no mask yet
@@ -290,18 +291,7 @@ cudaError_t launch_impl(const HhDecodeArgs& a, int sms, cudaStream_t stream) {
   if (smem > kMost || segments * c > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = allow_shared<swa_hh_decode_kernel<D>>(static_cast<int>(kMost));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
-  cfg.blockDim = dim3(kDecWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = c > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, swa_hh_decode_kernel<D>, a, c);
+  return launch_decode_cluster(swa_hh_decode_kernel<D>, a, segments, c, smem, stream);
 }
 
 }  // namespace

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(128)
                           uint8_t* kc, uint8_t* vc, uint8_t* sk, uint8_t* sv, int B, int Hkv, int W, int S) {
   constexpr int NG = D / kKv4Group;
   constexpr int ROW = kv4_row_bytes(D);
+  let_next_kernel_start();
   const long long r = (static_cast<long long>(blockIdx.x) * 128 + threadIdx.x) / kLanes;
   const int g = threadIdx.x % kLanes;
   uint2 x[NG] = {};

@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   const int G = a.G, W = a.W, S = a.S;
   const size_t head0 = static_cast<size_t>(b) * a.Hq + static_cast<size_t>(kvh) * G;
 
+  wait_for_previous_kernel();
   const int p = a.pos[b];
   const int n_ring = p < 0 ? 0 : (p < W ? p + 1 : W);
   const int n_sink = p < W ? 0 : min(p - W + 1, S);
@@ -371,18 +372,7 @@ cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   if (segments * c > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = allow_shared<swa_kv4_decode_kernel<D>>(static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(segments * c));
-  cfg.blockDim = dim3(kDecWarps * 32);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = c > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, swa_kv4_decode_kernel<D>, a, c);
+  return launch_decode_cluster(swa_kv4_decode_kernel<D>, a, segments, c, smem, stream);
 }
 
 }  // namespace
