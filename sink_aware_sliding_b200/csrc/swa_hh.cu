@@ -73,15 +73,16 @@ __global__ void __launch_bounds__(kAppendThreads)
 }
 
 // ---------------------------------------------------------------- fill
-// Select: one block per (b, KV head).  The `need` largest keys among the positions
-// S .. L - recent - 1 are found by a radix select on the ordered bits (11, 11 and 10
-// bits, histograms in shared memory): afterwards `cut` is the smallest kept key and
-// `ties` how many positions with exactly that key are kept, the earlier ones first.
-// Each warp then walks one contiguous stretch of positions, so that the kept ones come
-// out in ascending order after a prefix over the warps.  The keys are read from global
-// memory once, all loads in flight, and stay in shared memory for the five walks over
-// them (four prompts of 16384, 8 heads: 28 us with every walk in global memory); prompts
-// longer than that go by global memory, four loads a thread in flight.
+// Select: one block per (b, KV head).  The first S and the last `recent` positions get a key
+// above all scores; the largest of the other keys that have room are found by a radix select
+// (11, 11 and 10 bits, histograms in shared memory): afterwards `cut` is the smallest kept key
+// and `ties` how many positions with exactly that key are kept, the earlier ones first.  Each warp
+// then walks one contiguous stretch of positions, so that the kept ones come out in ascending
+// order after a prefix over the warps.  The keys are read from global memory once, all loads
+// in flight, and stay in shared memory for the five walks over them, four keys a thread and
+// step: the walks are what one SM can issue (four prompts of 16384, 8 heads: 28 us with every
+// walk in global memory, 16 us with a key a step; a cluster of blocks per head, which has to
+// add up their histograms, 37 us).  Longer prompts go by global memory.
 constexpr int kFillThreads = 1024;
 constexpr int kFillWarps = kFillThreads / 32;
 constexpr int kFillKeys = 49152;  // keys in shared memory (192 KB)
@@ -103,7 +104,7 @@ template <bool SMEM>
 __global__ void __launch_bounds__(kFillThreads)
     swa_hh_select_kernel(const float* __restrict__ score_in, int L, int32_t* slot_pos, float* score, int C, int S,
                          int recent) {
-  extern __shared__ uint32_t s_keys[];
+  extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ unsigned s_hist[2048];
   __shared__ unsigned s_warp[kFillWarps];
   __shared__ unsigned s_cut, s_left;
@@ -119,75 +120,90 @@ __global__ void __launch_bounds__(kFillThreads)
     }
     return;
   }
+  constexpr uint32_t kAlways = 0xffffffffu;
+  const int lo = S, hi = L - recent;  // positions outside stay in any case
+  const int quads = (L + 3) / 4;
+  auto key_of = [&](int i) -> uint32_t { return i < lo || i >= hi ? kAlways : order_bits(in[i]); };
   if constexpr (SMEM) {
 #pragma unroll 8
     for (int i = tid; i < L; i += kFillThreads) s_keys[i] = order_bits(in[i]);
+    if (tid < 4 * quads - L) s_keys[L + tid] = 0u;
+    __syncthreads();
+    for (int i = tid; i < lo + recent; i += kFillThreads) s_keys[i < lo ? i : hi + i - lo] = kAlways;
     __syncthreads();
   }
-  auto key_at = [&](int i) -> uint32_t {
-    if constexpr (SMEM) return s_keys[i];
-    return order_bits(in[i]);
+  // Four neighbouring keys.  Those behind the last position are 0, the lowest: they come after all others, so
+  // that no tie is given to them.
+  auto keys_at = [&](int q, uint32_t (&k)[4]) {
+    if constexpr (SMEM) {
+      const uint4 v = reinterpret_cast<const uint4*>(s_keys)[q];
+      k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = 4 * q + e < L ? key_of(4 * q + e) : 0u;
+    }
   };
-  const int lo = S, hi = L - recent;          // positions that compete
-  unsigned prefix = 0, need = C - S - recent;  // need <= hi - lo, as L > C
-  // need = 0: nothing competes successfully; cut above every key
-  unsigned cut = 0xffffffffu, ties = 0;
-  if (need > 0) {
-    constexpr int kShift[3] = {21, 10, 0};
-    constexpr int kBits[3] = {11, 11, 10};
+  const unsigned room = C - S - recent;  // fewer than the others, as L > C
+  unsigned cut = 0, need = room;         // prefix of the cut so far, keys wanted at or below it
+  constexpr int kShift[3] = {21, 10, 0};
+  constexpr int kBits[3] = {11, 11, 10};
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = kShift[pass];
-      const unsigned bins = 1u << kBits[pass];
-      for (unsigned i = tid; i < bins; i += kFillThreads) s_hist[i] = 0;
-      __syncthreads();
-#pragma unroll 4
-      for (int i = lo + tid; i < hi; i += kFillThreads) {
-        const uint32_t key = key_at(i);
-        if (pass == 0 || (key >> (shift + kBits[pass])) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
-      }
-      __syncthreads();
-      // from the top bin down, one or two neighbouring bins a thread
-      constexpr unsigned kPer[3] = {2, 2, 1};
-      unsigned n[2] = {0, 0};
+  for (int pass = 0; pass < 3; ++pass) {
+    if (room == 0) break;
+    const int shift = kShift[pass];
+    const unsigned bins = 1u << kBits[pass];
+    for (unsigned i = tid; i < bins; i += kFillThreads) s_hist[i] = 0;
+    __syncthreads();
+#pragma unroll 2
+    for (int q = tid; q < quads; q += kFillThreads) {
+      uint32_t k[4];
+      keys_at(q, k);
 #pragma unroll
-      for (unsigned i = 0; i < kPer[pass]; ++i) n[i] = s_hist[bins - 1 - (tid * kPer[pass] + i)];
-      unsigned above = block_prefix(n[0] + n[1], s_warp, lane, warp);
-#pragma unroll
-      for (unsigned i = 0; i < kPer[pass]; ++i) {
-        if (above < need && above + n[i] >= need) {  // one bin of one thread
-          s_cut = (prefix << kBits[pass]) | (bins - 1 - (tid * kPer[pass] + i));
-          s_left = need - above;
-        }
-        above += n[i];
-      }
-      __syncthreads();
-      prefix = s_cut;
-      need = s_left;
-      __syncthreads();
+      for (int e = 0; e < 4; ++e)
+        if (k[e] != kAlways && (pass == 0 || (k[e] >> (shift + kBits[pass])) == cut))
+          atomicAdd(&s_hist[(k[e] >> shift) & (bins - 1)], 1u);
     }
-    cut = prefix;
-    ties = need;
+    __syncthreads();
+    // from the top bin down, one or two neighbouring bins a thread
+    constexpr unsigned kPer[3] = {2, 2, 1};
+    unsigned n[2] = {0, 0};
+#pragma unroll
+    for (unsigned i = 0; i < kPer[pass]; ++i) n[i] = s_hist[bins - 1 - (tid * kPer[pass] + i)];
+    unsigned above = block_prefix(n[0] + n[1], s_warp, lane, warp);
+#pragma unroll
+    for (unsigned i = 0; i < kPer[pass]; ++i) {
+      if (above < need && above + n[i] >= need) {  // one bin of one thread
+        s_cut = (cut << kBits[pass]) | (bins - 1 - (tid * kPer[pass] + i));
+        s_left = need - above;
+      }
+      above += n[i];
+    }
+    __syncthreads();
+    cut = s_cut;
+    need = s_left;
+    __syncthreads();
   }
-  // ---- compaction: stretch of this warp
-  const int per = ((L + kFillWarps - 1) / kFillWarps + 31) / 32 * 32;
-  const int first = min(L, warp * per), last = min(L, first + per);
-  auto kind = [&](int i, bool& above, bool& equal) {
-    above = equal = false;
-    if (i < last) {
-      const bool always = i < lo || i >= hi;
-      const uint32_t key = key_at(i);
-      above = always || (ties > 0 && key > cut);
-      equal = !always && ties > 0 && key == cut;
-    }
+  // no room for others: the cut is the key of those that stay in any case
+  if (room == 0) cut = kAlways;
+  const int ties = room == 0 ? S + recent : static_cast<int>(need);
+  // ---- compaction: stretch of this warp, in quads
+  const int per = ((quads + kFillWarps - 1) / kFillWarps + 31) / 32 * 32;
+  const int first = min(quads, warp * per), last = min(quads, first + per);
+  // this lane's quad: how many lie above the cut (low half) and on it (high half)
+  auto count = [&](const uint32_t (&k)[4]) {
+    unsigned n = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) n += k[e] > cut ? 1u : k[e] == cut ? 0x10000u : 0u;
+    return n;
   };
   int n_kept = 0, n_ties = 0;
-#pragma unroll 4
-  for (int i0 = first; i0 < last; i0 += 32) {
-    bool above, equal;
-    kind(i0 + lane, above, equal);
-    n_kept += above;
-    n_ties += equal;
+#pragma unroll 2
+  for (int q = first + lane; q < last; q += 32) {
+    uint32_t k[4];
+    keys_at(q, k);
+    const unsigned n = count(k);
+    n_kept += n & 0xffffu;
+    n_ties += n >> 16;
   }
   n_kept = __reduce_add_sync(kFull, n_kept);
   n_ties = __reduce_add_sync(kFull, n_ties);
@@ -199,25 +215,38 @@ __global__ void __launch_bounds__(kFillThreads)
   // kept without ties, and ties, in the stretches before
   int out = __reduce_add_sync(kFull, lane < warp ? s_kept[lane] : 0);
   int tie = __reduce_add_sync(kFull, lane < warp ? s_ties[lane] : 0);
-#pragma unroll 4
-  for (int i0 = first; i0 < last; i0 += 32) {
-    const int i = i0 + lane;
-    bool above, equal;
-    kind(i, above, equal);
-    const unsigned ma = __ballot_sync(kFull, above), me = __ballot_sync(kFull, equal);
-    const unsigned below = (1u << lane) - 1;
-    const int my_tie = tie + __popc(me & below);
-    const int slot = out + __popc(ma & below) + min(my_tie, static_cast<int>(ties));
-    if (above || (equal && my_tie < static_cast<int>(ties))) {
-      sp[slot] = i;
-      // the key gives the score back, but for NaN and the zeros' signs
-      const uint32_t key = key_at(i);
-      sc[slot] = !SMEM || key == 0u || key == 0x80000000u ? in[i]
-                 : __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+  for (int q0 = first; q0 < last; q0 += 32) {
+    const int q = q0 + lane;
+    uint32_t k[4] = {0u, 0u, 0u, 0u};
+    unsigned n = 0;
+    if (q < last) {
+      keys_at(q, k);
+      n = count(k);
     }
-    out += __popc(ma);
-    tie += __popc(me);
+    unsigned incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    int my_tie = tie + static_cast<int>((incl - n) >> 16);
+    int slot = out + static_cast<int>((incl - n) & 0xffffu) + min(my_tie, ties);
+    if (n != 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool equal = k[e] == cut;
+        if (k[e] > cut || (equal && my_tie < ties)) {
+          sp[slot++] = 4 * q + e;
+        }
+        my_tie += equal;
+      }
+    }
+    const unsigned total = __shfl_sync(kFull, incl, 31);
+    out += total & 0xffffu;
+    tie += total >> 16;
   }
+  __syncthreads();
+  for (int i = tid; i < C; i += kFillThreads) sc[i] = in[sp[i]];  // all C slots are taken
 }
 
 // Copy the chosen rows, one thread per 16 bytes, `per` blocks a (b, KV head).
@@ -255,7 +284,7 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
   const int segs = B * Hkv;
   cudaError_t e = cudaSuccess;
   if (L <= kFillKeys) {
-    const size_t smem = L > C ? static_cast<size_t>(L) * 4 : 0;
+    const size_t smem = L > C ? static_cast<size_t>((L + 3) / 4) * 16 : 0;
     e = allow_shared<swa_hh_select_kernel<true>>(kFillKeys * 4);
     if (e != cudaSuccess) return e;
     swa_hh_select_kernel<true><<<segs, kFillThreads, smem, stream>>>(score_in, L, slot_pos, score, C, S, recent);
