@@ -304,3 +304,71 @@ def test_captured_and_on_two_streams():
     for st in (a, b):
         for x, y in zip(st[0] + [st[1], st[2]], want[0] + [want[1], want[2]]):
             assert torch.equal(x, y)
+
+
+def test_scores_wait_that_runs_out_is_reported_and_leaves_the_library_usable():
+    """The load warp issues nothing (test hook): every wait ends at its limit, the status says so, and the next call
+    works."""
+    B, L, H, d = 1, 300, 2, 128
+    q, k = rand((B, L, H, d), 1).cuda(), rand((B, L, H, d), 2).cuda()
+    lse = torch.empty(B, H, L, device="cuda")
+    swa.swa_fwd(q, k, k, torch.empty_like(q), lse, L, 0)
+    want, got = torch.empty(B, H, L, device="cuda"), torch.empty(B, H, L, device="cuda")
+    swa.swa_hh_scores(q, k, lse, want, L, L, 0)
+    assert swa.swa_device_error() == 0
+    old = swa.swa_set_wait_timeout_ns(2_000_000)
+    swa.swa_set_debug_flags(1)
+    try:
+        swa.swa_hh_scores(q, k, lse, got, L, L, 0)
+        assert swa.swa_device_error() == swa.SWA_ERR_DEVICE_TIMEOUT
+    finally:
+        swa.swa_set_debug_flags(0)
+        swa.swa_set_wait_timeout_ns(old)
+    swa.swa_hh_scores(q, k, lse, got, L, L, 0)
+    assert swa.swa_device_error() == 0 and torch.equal(got, want)
+
+
+def test_scores_captured_twice_and_replayed_in_turn():
+    """Two graphs of the same call on different inputs share nothing."""
+    B, L, H, d = 1, 260, 2, 64
+    sets = []
+    for s in (1, 5):
+        q, k = rand((B, L, H, d), s).cuda(), rand((B, L, H, d), s + 1).cuda()
+        lse, score = torch.empty(B, H, L, device="cuda"), torch.empty(B, H, L, device="cuda")
+        swa.swa_fwd(q, k, k, torch.empty_like(q), lse, L, 0)
+        swa.swa_hh_scores(q, k, lse, score, 100, L, 0)
+        sets.append((q, k, lse, score, score.clone()))
+    torch.cuda.synchronize()
+    graphs = []
+    for q, k, lse, score, _ in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            swa.swa_hh_scores(q, k, lse, score, 100, L, 0)
+        graphs.append(g)
+    for _ in range(3):
+        for (_, _, _, score, _), g in zip(sets, graphs):
+            score.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for _, _, _, score, want in sets:
+        assert torch.equal(score, want)
+
+
+def test_calls_on_a_stream_given_by_hand_and_without_sequences():
+    st = torch.cuda.Stream()
+    k, v, sp, s = cache(2, 2, 64, 64, 3, 1.0)
+    args = [t.cuda() for t in (k, v)] + [torch.from_numpy(sp).cuda(), torch.from_numpy(s).cuda()]
+    q = rand((2, 4, 64), 4).cuda()
+    outs = [torch.zeros(2, 4, 64, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    swa.swa_hh_decode(q, *args, outs[0], None, stream=st)
+    st.synchronize()
+    args[3].copy_(torch.from_numpy(s))
+    swa.swa_hh_decode(q, *args, outs[1], None)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and float(outs[0].abs().sum()) > 0
+    none = [t[:0] for t in args]
+    swa.swa_hh_decode(q[:0], *none, outs[0][:0], None)
+    swa.swa_hh_cache_append(k[:0, :, 0].contiguous().cuda(), v[:0, :, 0].contiguous().cuda(),
+                            torch.zeros(0, dtype=torch.int32, device="cuda"), *none, None, 0, 1)
+    torch.cuda.synchronize()

@@ -269,3 +269,45 @@ def test_captured_and_on_two_streams():
     torch.cuda.synchronize()
     assert torch.equal(out, alone[0][0]) and torch.equal(lse, alone[0][1])
     assert torch.equal(ob, alone[1][0]) and torch.equal(lb, alone[1][1])
+
+
+def test_many_sequences_and_repeated_calls_agree_bit_for_bit():
+    """A decode's sums are taken in an order that the sizes give: the same call gives the same bits."""
+    B, H, Hq, d, W, S = 70, 3, 6, 64, 90, 2
+    c, kv, vv = filled(B, H, d, W, S, 71)
+    q = rand((B, Hq, d), 72)
+    check_decode(c, q, [(37 * b) % 200 for b in range(B)], kv, vv)
+    pos = torch.tensor([(37 * b) % 200 for b in range(B)], dtype=torch.int32, device="cuda")
+    outs = [torch.empty(B, Hq, d, device="cuda") for _ in range(3)]
+    for o in outs:
+        swa.swa_kv4_decode(q.cuda(), *c.args(), pos, o, None, W, S)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_constant_rows_of_any_size():
+    """Groups of one value have step 0 and carry it in their minimum: the output is that value."""
+    B, H, Hq, d, W = 1, 1, 8, 128, 40
+    for value in (3.0, -1e9, 1e25, 0.0):
+        c = Cache(B, H, d, W, 0)
+        v = torch.full((B, W, H, d), value).bfloat16()
+        swa.swa_kv4_cache_fill(rand((B, W, H, d), 1).cuda(), v.cuda(), *c.args(), W, 0)
+        out = torch.empty(B, Hq, d, device="cuda")
+        swa.swa_kv4_decode(rand((B, Hq, d), 2).cuda(), *c.args(), torch.full((1,), W - 1, dtype=torch.int32,
+                                                                            device="cuda"), out, None, W, 0)
+        want = float(v[0, 0, 0, 0])
+        # the two bf16 parts of the softmax numerators leave 2^-16, the sums 40 * 2^-24
+        assert float((out - want).abs().max()) <= (2.0 ** -16 + 40 * 2.0 ** -24 + 2.0 ** -20) * abs(want)
+
+
+def test_a_prompt_that_fills_the_ring_many_times_over_and_a_wide_batch():
+    """More sequences than blocks in z, and positions that wrap the ring several times."""
+    B, P, H, d, W, S = 300, 23, 1, 64, 5, 2
+    k, v = rand((B, P, H, d), 81), rand((B, P, H, d), 82)
+    c = Cache(B, H, d, W, S)
+    swa.swa_kv4_cache_fill(k.cuda(), v.cuda(), *c.args(), W, S)
+    torch.cuda.synchronize()
+    rows = oracle.kv4_pack(k)
+    for p in range(P - W, P):
+        np.testing.assert_array_equal(c.kc[:, :, p % W].cpu().numpy(), rows[:, p])
+    np.testing.assert_array_equal(c.sk.cpu().numpy()[:, 0], rows[:, :S, 0])
