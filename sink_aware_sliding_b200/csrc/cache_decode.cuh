@@ -3,8 +3,8 @@
 // states over the warps of a block and the blocks of a cluster.
 //
 // One cluster of blocks works on one (sequence, KV head).  Its keys are cut into
-// tiles of 16; warp w of the cluster takes the tiles w, w + n, w + 2 n, ...  Each
-// warp copies its tiles into shared memory several tiles ahead (cp.async, no block
+// tiles; warp w of the cluster takes the tiles w, w + n, w + 2 n, ...  Each
+// warp copies its tiles into shared memory one or two tiles ahead (cp.async, no block
 // barrier in the loop) and keeps (reference, sum, O) of its keys for up to eight
 // query heads.  The partial states meet in shared memory, first over the warps,
 // then over the cluster: no workspace, no second launch, and a sum whose order
@@ -21,7 +21,7 @@
 namespace swa {
 
 constexpr int kDecWarps = 4;    // warps per block
-constexpr int kDecTile = 16;    // keys per tile
+constexpr int kDecTile = 16;    // keys per product
 constexpr int kDecHeads = 8;    // query heads per KV head, at most
 
 // The caches' rows are read once a step, so they leave the L2 first: what the block
@@ -211,8 +211,8 @@ cudaError_t launch_decode_cluster(Kernel kernel, const Args& a, long long segmen
   return cudaLaunchKernelEx(&cfg, kernel, a, c);
 }
 
-// Blocks per cluster: enough that `segments` fill the GPU about `waves` times over,
-// but at least kDecWarps tiles for each block and at most 8 (the portable size).
+// Blocks per cluster: a power of two, enough that `segments` fill the GPU `waves` times over,
+// but with two tiles for each warp and at most 8 (the portable size).
 inline int decode_cluster(long long segments, long long tiles, int sms, int blocks_per_sm, int waves) {
   int c = 1;
   while (c < 8 && segments * c < static_cast<long long>(sms) * blocks_per_sm * waves &&

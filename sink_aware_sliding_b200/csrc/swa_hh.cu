@@ -76,13 +76,14 @@ __global__ void __launch_bounds__(kAppendThreads)
 // Select: one block per (b, KV head).  The first S and the last `recent` positions get a key
 // above all scores; the largest of the other keys that have room are found by a radix select
 // (11, 11 and 10 bits, histograms in shared memory): afterwards `cut` is the smallest kept key
-// and `ties` how many positions with exactly that key are kept, the earlier ones first.  Each warp
-// then walks one contiguous stretch of positions, so that the kept ones come out in ascending
+// and `ties` how many positions with exactly that key are kept, the earlier ones first.  Each
+// warp then walks one contiguous stretch of positions, so that the kept ones come out in ascending
 // order after a prefix over the warps.  The keys are read from global memory once, all loads
 // in flight, and stay in shared memory for the five walks over them, four keys a thread and
 // step: the walks are what one SM can issue (four prompts of 16384, 8 heads: 28 us with every
-// walk in global memory, 16 us with a key a step; a cluster of blocks per head, which has to
-// add up their histograms, 37 us).  Longer prompts go by global memory.
+// walk in global memory, 13.5 us with a key a step, 11.5 us so; a cluster of blocks per head,
+// which has to add up their histograms, 37 us).  Copying the rows takes as long again.  Longer
+// prompts go by global memory.
 constexpr int kFillThreads = 1024;
 constexpr int kFillWarps = kFillThreads / 32;
 constexpr int kFillKeys = 49152;  // keys in shared memory (192 KB)

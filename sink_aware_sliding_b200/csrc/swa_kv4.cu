@@ -11,6 +11,11 @@
 // first: seen as [d/32, 8, 4] the elements are stored in the order [8, d/32, 4], so
 // that 1/8 of the code bytes holds four neighbouring elements of every group, which
 // is what one thread of the decode kernel multiplies.
+//
+// Bound by instruction issue (76% of the slots in the fill, ALU pipe 59%): 63 instructions a
+// row.  Four prompts' last 4096 positions and 4 sinks, 8 heads, d = 128 (88 MB each way):
+// fill 21 us, 4.2 TB/s, read 20.5 us; with 16 lanes a row 27 and 23.5 us, with 64-bit
+// divisions for the row's place 41 and 31 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -8,10 +8,21 @@
 // 16 n 2^-24, so that "unpacking" is one AND per two elements and loses nothing.  q is
 // scaled by a power of two per head into fp16 (exact for all but elements 2^-28 below
 // the head's largest), and the odd nibbles' factor 16 goes into q and, for V, into the
-// final scaling.  Scores, steps and minima are applied in fp32.  p a_j is the one value
-// that is rounded, to fp16 (relative 2^-12): softmax numerators in 16 bits as in the
+// final scaling.  Steps are applied in fp32; minima times the sums of q, and times P, are
+// products as well, with the sums in three bf16 parts and P in two.  p a_j is the one value
+// that is rounded coarsely, to fp16 (2^-11): softmax numerators in 16 bits as in the
 // bf16 decode, with the running reference chosen so that p a_j stays below 2^15
-// whatever the steps are; the minima's part, sum p b_j, stays in fp32.
+// whatever the steps are.
+//
+// Keys are the 16 rows of the products and up to eight query heads their columns: half the
+// products of the other orientation, and the codes go into the operand's registers as they
+// are masked; the scores are turned through shared memory (one 1 KB tile a warp) to become
+// an operand of P V.  Bound by instruction issue, masks and permutes above all (ALU pipe 57%,
+// issue 59% over a launch with its tail), next to HBM: 293 instructions per 16 keys and warp.
+// B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 66 us,
+// 5.1 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
+// 75 us with the keys as rows, 66 us with 32 keys a step.  Under a power cap that lowers the
+// clock to 1.7 GHz it takes 73 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,9 +37,9 @@ namespace swa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kStages = 2;
-constexpr int kRows = 32;  // keys per tile: two products of 16 rows share a step of the softmax
-constexpr int kBlocksPerSm = 4;
+constexpr int kStages = 2;       // one tile is worked on while the next one comes: 80 KB in flight on an SM
+constexpr int kRows = 32;        // keys per tile: two products of 16 rows share a step of the softmax
+constexpr int kBlocksPerSm = 4;  // 16 warps: what 128 registers a thread allow
 
 template <int D>
 struct K4 {
@@ -368,6 +379,8 @@ cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   const size_t smem = kDecWarps * K4<D>::WARP;
   const long long segments = static_cast<long long>(a.B) * a.Hkv;
   const long long tiles = (static_cast<long long>(a.W) + a.S + kRows - 1) / kRows;
+  // 512 segments: 73 us with one block each (3.5 on an SM: some have 4), 66 us with two, 84 us with four, whose
+  // starts and merges weigh more
   const int c = decode_cluster(segments, tiles, sms, kBlocksPerSm, 1);
   if (segments * c > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = allow_shared<swa_kv4_decode_kernel<D>>(static_cast<int>(smem));
