@@ -437,7 +437,7 @@ def swa_kv4_cache_fill(k, v, kcache, vcache, sink_k, sink_v, window: int, n_sink
     B, P, Hkv, d = shape = k.shape
     kp, vp = _at(k, "k", _torch.bfloat16, shape, dev), _at(v, "v", _torch.bfloat16, shape, dev)
     cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, window, n_sink, _on(stream, dev))
+    st = _load().swa_kv4_cache_fill(kp, vp, P, *cache, B, Hkv, d, int(window), int(n_sink), _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_fill")
 
@@ -451,7 +451,7 @@ def swa_kv4_cache_append(k_new, v_new, pos, kcache, vcache, sink_k, sink_v, wind
     kp, vp = _at(k_new, "k_new", _torch.bfloat16, shape, dev), _at(v_new, "v_new", _torch.bfloat16, shape, dev)
     pp = _at(pos, "pos", _torch.int32, (B,), dev)
     cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, window, n_sink, _on(stream, dev))
+    st = _load().swa_kv4_cache_append(kp, vp, pp, *cache, B, Hkv, d, int(window), int(n_sink), _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_append")
 
@@ -466,7 +466,7 @@ def swa_kv4_cache_read(positions, kcache, vcache, sink_k, sink_v, k_out, v_out, 
     pp = _at(positions, "positions", _torch.int32, (B, n), dev)
     cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
     code = SWA_DTYPE_F32 if k_out.dtype is _torch.float32 else SWA_DTYPE_BF16
-    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, window, n_sink, _on(stream, dev))
+    st = _load().swa_kv4_cache_read(pp, n, *cache, ko, vo, code, B, Hkv, d, int(window), int(n_sink), _on(stream, dev))
     if st:
         _check(st, "swa_kv4_cache_read")
 
@@ -495,7 +495,7 @@ def swa_kv4_decode(q, kcache, vcache, sink_k, sink_v, pos, out, lse, window: int
     Hkv = kcache.shape[1]
     pp = _at(pos, "pos", _torch.int32, (B,), dev)
     cache = _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink)
-    st = _load().swa_kv4_decode(qp, *cache, pp, op, lp, B, Hq, Hkv, d, window, n_sink, _scale(scale, d), code,
+    st = _load().swa_kv4_decode(qp, *cache, pp, op, lp, B, Hq, Hkv, d, int(window), int(n_sink), _scale(scale, d), code,
                                 _on(stream, dev))
     if st:
         _check(st, "swa_kv4_decode")
@@ -510,8 +510,8 @@ def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=
     Hkv = k.shape[2]
     st = _load().swa_hh_scores(_at(q, "q", _torch.bfloat16, q.shape, dev), _at(k, "k", _torch.bfloat16, (B, L, Hkv, d), dev),
                                _at(lse, "lse", _torch.float32, (B, Hq, L), dev),
-                               _at(score, "score", _torch.float32, (B, Hkv, L), dev), B, Hq, Hkv, L, d, n_obs, window,
-                               n_sink, _scale(scale, d), _on(stream, dev))
+                               _at(score, "score", _torch.float32, (B, Hkv, L), dev), B, Hq, Hkv, L, d, int(n_obs),
+                               int(window), int(n_sink), _scale(scale, d), _on(stream, dev))
     if st:
         _check(st, "swa_hh_scores")
 
@@ -533,7 +533,7 @@ def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: i
     C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
     st = _load().swa_hh_cache_fill(_at(k, "k", _torch.bfloat16, shape, dev), _at(v, "v", _torch.bfloat16, shape, dev),
                                    _at(score_in, "score_in", _torch.float32, (B, Hkv, L), dev), L, *cache, B, Hkv, d, C,
-                                   n_sink, recent, _on(stream, dev))
+                                   int(n_sink), int(recent), _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_fill")
 
@@ -549,7 +549,7 @@ def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot
     st = _load().swa_hh_cache_append(_at(k_new, "k_new", _torch.bfloat16, shape, dev),
                                      _at(v_new, "v_new", _torch.bfloat16, shape, dev), _at(pos, "pos", _torch.int32, (B,), dev),
                                      *cache, None if slot is None else _at(slot, "slot", _torch.int32, (B, Hkv), dev), B, Hkv,
-                                     d, C, n_sink, recent, _on(stream, dev))
+                                     d, C, int(n_sink), int(recent), _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_append")
 
@@ -562,7 +562,7 @@ def swa_hh_decode(q, kcache, vcache, slot_pos, score, out, lse, scale=None, deca
     _need(kcache.dim() == 4, "kcache [B, Hkv, capacity, d]")
     Hkv = kcache.shape[1]
     C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
-    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), decay, code, _on(stream, dev))
+    st = _load().swa_hh_decode(qp, *cache, op, lp, B, Hq, Hkv, d, C, _scale(scale, d), float(decay), code, _on(stream, dev))
     if st:
         _check(st, "swa_hh_decode")
 
@@ -597,7 +597,7 @@ def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_b
     pp = _at(positions, "positions", _torch.int32, (n_axes, T), dev)
     sec = (ctypes.c_int32 * max(1, n_axes))(*sections)
     st = _load().swa_rope_axes_qk(qp, kp, pp, T, Hq, Hkv, d, qs, ks, sec, n_axes, _ROPE_LAYOUTS[layout],
-                                  rope_base, 1 if inverse else 0,
+                                  float(rope_base), 1 if inverse else 0,
                                   SWA_DTYPE_F32 if q.dtype is _torch.float32 else SWA_DTYPE_BF16, _on(stream, dev))
     if st:
         _check(st, "swa_rope_axes_qk")
