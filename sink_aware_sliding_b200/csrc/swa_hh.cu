@@ -101,10 +101,30 @@ __device__ __forceinline__ unsigned block_prefix(unsigned mine, unsigned* s_warp
   return __reduce_add_sync(kFull, lane < warp ? s_warp[lane] : 0u) + incl - mine;
 }
 
+// The rows of a cache to fill; `here`: the selecting block copies them itself.
+struct FillRows {
+  const uint4* k;
+  const uint4* v;
+  uint4* kc;
+  uint4* vc;
+  int Hkv, vec, kept;
+  bool here;
+};
+
+// 16 bytes number i of a (b, KV head)'s chosen rows, K's and V's.
+__device__ __forceinline__ void copy_unit(const FillRows& f, size_t seg, int L, int C, int i, const int32_t* sp) {
+  const int s = i / f.vec, e = i - s * f.vec;
+  const size_t b = seg / f.Hkv, h = seg % f.Hkv;
+  const size_t src = ((b * L + sp[s]) * f.Hkv + h) * f.vec + e;
+  const size_t dst = (seg * C + s) * f.vec + e;
+  f.kc[dst] = f.k[src];
+  f.vc[dst] = f.v[src];
+}
+
 template <bool SMEM>
 __global__ void __launch_bounds__(kFillThreads)
     swa_hh_select_kernel(const float* __restrict__ score_in, int L, int32_t* slot_pos, float* score, int C, int S,
-                         int recent) {
+                         int recent, const __grid_constant__ FillRows rows) {
   extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ unsigned s_hist[2048];
   __shared__ unsigned s_warp[kFillWarps];
@@ -118,6 +138,11 @@ __global__ void __launch_bounds__(kFillThreads)
     for (int i = tid; i < C; i += kFillThreads) {
       sp[i] = i < L ? i : -1;
       sc[i] = i < L ? in[i] : 0.f;
+    }
+    if (rows.here) {
+      __syncthreads();
+#pragma unroll 4
+      for (int i = tid; i < rows.kept * rows.vec; i += kFillThreads) copy_unit(rows, blockIdx.x, L, C, i, sp);
     }
     return;
   }
@@ -248,24 +273,20 @@ __global__ void __launch_bounds__(kFillThreads)
   }
   __syncthreads();
   for (int i = tid; i < C; i += kFillThreads) sc[i] = in[sp[i]];  // all C slots are taken
+  if (rows.here) {
+#pragma unroll 4
+    for (int i = tid; i < rows.kept * rows.vec; i += kFillThreads) copy_unit(rows, blockIdx.x, L, C, i, sp);
+  }
 }
 
 // Copy the chosen rows, one thread per 16 bytes, `per` blocks a (b, KV head).
 __global__ void __launch_bounds__(256)
-    swa_hh_gather_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v, int L, uint4* __restrict__ kc,
-                         uint4* __restrict__ vc, const int32_t* __restrict__ slot_pos, int Hkv, int vec, int C,
-                         int kept, int per) {
+    swa_hh_gather_kernel(const __grid_constant__ FillRows rows, int L, const int32_t* __restrict__ slot_pos, int C,
+                         int per) {
   const size_t seg = blockIdx.x / per;
-  const size_t b = seg / Hkv, h = seg % Hkv;
-  const int total = kept * vec;
-  for (int i = blockIdx.x % per * 256 + threadIdx.x; i < total; i += per * 256) {
-    const int s = i / vec, e = i % vec;
-    const int p = slot_pos[seg * C + s];
-    const size_t src = ((b * L + p) * Hkv + h) * vec + e;
-    const size_t dst = (seg * C + s) * vec + e;
-    kc[dst] = k[src];
-    vc[dst] = v[src];
-  }
+  const int total = rows.kept * rows.vec;
+  for (int i = blockIdx.x % per * 256 + threadIdx.x; i < total; i += per * 256)
+    copy_unit(rows, seg, L, C, i, slot_pos + seg * C);
 }
 
 }  // namespace
@@ -283,25 +304,27 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
                            int32_t* slot_pos, float* score, int B, int Hkv, int d, int C, int S, int recent, int sms,
                            cudaStream_t stream) {
   const int segs = B * Hkv;
+  const int kept = std::min(L, C), vec = d / 8;
+  // The selecting block copies the rows as well where they are few, which spares the caller a launch (3 us; 128 KB
+  // each of 8 heads: 8.7 us on the GPU against 7.2 us), or where there is a block for most SMs (256 heads: 33.5 against
+  // 36.7 us); else a kernel of its own does (512 KB each of 8 heads: 10.7 us against 20.1 us).
+  const bool here = static_cast<long long>(kept) * vec * 32 <= (132 << 10) || segs >= sms * 7 / 8;
+  const FillRows rows{static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<uint4*>(kc),
+                      static_cast<uint4*>(vc), Hkv, vec, kept, here};
   cudaError_t e = cudaSuccess;
   if (L <= kFillKeys) {
     const size_t smem = L > C ? static_cast<size_t>((L + 3) / 4) * 16 : 0;
     e = allow_shared<swa_hh_select_kernel<true>>(kFillKeys * 4);
     if (e != cudaSuccess) return e;
-    swa_hh_select_kernel<true><<<segs, kFillThreads, smem, stream>>>(score_in, L, slot_pos, score, C, S, recent);
+    swa_hh_select_kernel<true><<<segs, kFillThreads, smem, stream>>>(score_in, L, slot_pos, score, C, S, recent, rows);
   } else {
-    swa_hh_select_kernel<false><<<segs, kFillThreads, 0, stream>>>(score_in, L, slot_pos, score, C, S, recent);
+    swa_hh_select_kernel<false><<<segs, kFillThreads, 0, stream>>>(score_in, L, slot_pos, score, C, S, recent, rows);
   }
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int kept = std::min(L, C);
-  if (kept == 0) return cudaSuccess;
-  const int vec = d / 8;
+  if (e != cudaSuccess || kept == 0 || here) return e;
   const int blocks = (kept * vec + 255) / 256;
-  const int x = std::min(blocks, std::max(1, (sms * 32 + segs - 1) / segs));
-  swa_hh_gather_kernel<<<static_cast<unsigned>(x) * segs, 256, 0, stream>>>(
-      static_cast<const uint4*>(k), static_cast<const uint4*>(v), L, static_cast<uint4*>(kc), static_cast<uint4*>(vc),
-      slot_pos, Hkv, vec, C, kept, x);
+  const int per = std::min(blocks, std::max(1, (sms * 32 + segs - 1) / segs));
+  swa_hh_gather_kernel<<<static_cast<unsigned>(per) * segs, 256, 0, stream>>>(rows, L, slot_pos, C, per);
   return cudaGetLastError();
 }
 
