@@ -111,14 +111,38 @@ struct FillRows {
   bool here;
 };
 
-// 16 bytes number i of a (b, KV head)'s chosen rows, K's and V's.
-__device__ __forceinline__ void copy_unit(const FillRows& f, size_t seg, int L, int C, int i, const int32_t* sp) {
-  const int s = i / f.vec, e = i - s * f.vec;
-  const size_t b = seg / f.Hkv, h = seg % f.Hkv;
-  const size_t src = ((b * L + sp[s]) * f.Hkv + h) * f.vec + e;
-  const size_t dst = (seg * C + s) * f.vec + e;
-  f.kc[dst] = f.k[src];
-  f.vc[dst] = f.v[src];
+// Copies the 16 bytes number first, first + step, ... of a (b, KV head)'s chosen rows, K's and V's.
+__device__ __forceinline__ void copy_rows(const FillRows& f, size_t seg, int L, int C, const int32_t* sp, int first,
+                                          int step) {
+  const size_t src0 = (seg / f.Hkv * L * f.Hkv + seg % f.Hkv) * f.vec, dst0 = seg * C * f.vec;
+  const size_t row = static_cast<size_t>(f.Hkv) * f.vec;
+  const int total = f.kept * f.vec;
+  const uint4* __restrict__ k = f.k + src0;
+  const uint4* __restrict__ v = f.v + src0;
+  uint4* __restrict__ kc = f.kc + dst0;
+  uint4* __restrict__ vc = f.vc + dst0;
+  constexpr int kBatch = 2;  // units in flight
+  for (int i0 = first; i0 < total; i0 += kBatch * step) {
+    uint4 x[kBatch], y[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * step;
+      if (i < total) {
+        const int s = i / f.vec, e = i - s * f.vec;
+        const size_t src = sp[s] * row + e;
+        x[u] = k[src];
+        y[u] = v[src];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * step;
+      if (i < total) {
+        kc[i] = x[u];
+        vc[i] = y[u];
+      }
+    }
+  }
 }
 
 template <bool SMEM>
@@ -141,8 +165,7 @@ __global__ void __launch_bounds__(kFillThreads)
     }
     if (rows.here) {
       __syncthreads();
-#pragma unroll 4
-      for (int i = tid; i < rows.kept * rows.vec; i += kFillThreads) copy_unit(rows, blockIdx.x, L, C, i, sp);
+      copy_rows(rows, blockIdx.x, L, C, sp, tid, kFillThreads);
     }
     return;
   }
@@ -273,10 +296,7 @@ __global__ void __launch_bounds__(kFillThreads)
   }
   __syncthreads();
   for (int i = tid; i < C; i += kFillThreads) sc[i] = in[sp[i]];  // all C slots are taken
-  if (rows.here) {
-#pragma unroll 4
-    for (int i = tid; i < rows.kept * rows.vec; i += kFillThreads) copy_unit(rows, blockIdx.x, L, C, i, sp);
-  }
+  if (rows.here) copy_rows(rows, blockIdx.x, L, C, sp, tid, kFillThreads);
 }
 
 // Copy the chosen rows, one thread per 16 bytes, `per` blocks a (b, KV head).
@@ -284,9 +304,7 @@ __global__ void __launch_bounds__(256)
     swa_hh_gather_kernel(const __grid_constant__ FillRows rows, int L, const int32_t* __restrict__ slot_pos, int C,
                          int per) {
   const size_t seg = blockIdx.x / per;
-  const int total = rows.kept * rows.vec;
-  for (int i = blockIdx.x % per * 256 + threadIdx.x; i < total; i += per * 256)
-    copy_unit(rows, seg, L, C, i, slot_pos + seg * C);
+  copy_rows(rows, seg, L, C, slot_pos + seg * C, blockIdx.x % per * 256 + threadIdx.x, per * 256);
 }
 
 }  // namespace
@@ -306,7 +324,7 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
   const int segs = B * Hkv;
   const int kept = std::min(L, C), vec = d / 8;
   // The selecting block copies the rows as well where they are few, which spares the caller a launch (3 us; 128 KB
-  // each of 8 heads: 8.7 us on the GPU against 7.2 us), or where there is a block for most SMs (256 heads: 33.5 against
+  // each of 8 heads: 8.7 us on the GPU against 7.2 us), or where there is a block for most SMs (256 heads: 31.6 against
   // 36.7 us); else a kernel of its own does (512 KB each of 8 heads: 10.7 us against 20.1 us).
   const bool here = static_cast<long long>(kept) * vec * 32 <= (132 << 10) || segs >= sms * 7 / 8;
   const FillRows rows{static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<uint4*>(kc),
