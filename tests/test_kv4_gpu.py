@@ -311,3 +311,56 @@ def test_a_prompt_that_fills_the_ring_many_times_over_and_a_wide_batch():
     for p in range(P - W, P):
         np.testing.assert_array_equal(c.kc[:, :, p % W].cpu().numpy(), rows[:, p])
     np.testing.assert_array_equal(c.sk.cpu().numpy()[:, 0], rows[:, :S, 0])
+
+
+def test_captured_behind_copies_and_a_join_of_streams():
+    """The decode may start before the kernel in front of it ends; behind a copy, a memset, an event of another stream
+    or at a graph's very start there is none, and it has to wait for those all the same."""
+    B, H, Hq, d, W, S = 2, 2, 8, 128, 500, 4
+    c, _, _ = filled(B, H, d, W, S, 91)
+    q = rand((B, Hq, d), 92).cuda()
+    pos = torch.tensor([600, 77], dtype=torch.int32, device="cuda")
+    want = torch.empty(B, Hq, d, device="cuda")
+    swa.swa_kv4_decode(q, *c.args(), pos, want, None, W, S)
+    torch.cuda.synchronize()
+    qin, pin = torch.zeros_like(q), torch.zeros_like(pos)
+    big, host = torch.zeros(64 << 20, device="cuda"), q.cpu().pin_memory()
+    outs = [torch.zeros(B, Hq, d, device="cuda") for _ in range(4)]
+    side = torch.cuda.Stream()
+
+    def copied(out):
+        qin.copy_(host, non_blocking=True)
+        pin.copy_(pos)
+        swa.swa_kv4_decode(qin, *c.args(), pin, out, None, W, S)
+
+    def behind_a_kernel(out):
+        big.add_(1.0)  # takes longer than a launch
+        qin.copy_(q * 1.0)
+        swa.swa_kv4_decode(qin, *c.args(), pos, out, None, W, S)
+
+    def joined(out):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.add_(1.0)
+            qin.copy_(q * 1.0)
+        pin.copy_(pos)
+        torch.cuda.current_stream().wait_stream(side)
+        swa.swa_kv4_decode(qin, *c.args(), pin, out, None, W, S)
+
+    def alone(out):
+        swa.swa_kv4_decode(q, *c.args(), pos, out, None, W, S)
+
+    for f, out in zip((copied, behind_a_kernel, joined, alone), outs):
+        f(out)  # eagerly
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), f.__name__
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            f(out)
+        for _ in range(3):
+            qin.zero_()
+            pin.zero_()
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want), f.__name__
