@@ -371,7 +371,8 @@ int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const 
  *     score          [B, Hkv, capacity] float32   weight the slot has accumulated
  * An empty cache is slot_pos filled with -1 and score with 0.
  * Requires n_sink >= 0, recent >= 1, capacity >= n_sink + recent.
- * Supported: d in {64, 128}, capacity <= 16384.
+ * Supported: d in {64, 128}, capacity <= 16384.  Tensors of rows are 16-byte aligned,
+ * pos, slot, slot_pos, lse and the scores 4-byte.
  *
  * swa_hh_scores: the weight each key of a prompt received from the last n_obs queries,
  *     score[b, h, j] = sum over t in [L - n_obs, L), query heads g of KV head h, with
@@ -460,8 +461,8 @@ int swa_debug_error_word(swa_stream_t stream);
 unsigned long long swa_set_wait_timeout_ns(unsigned long long ns);
 
 /*
- * Test hooks, process-wide.  Bit 0 makes the prefill kernels' load warp issue
- * no copies, so that its consumers' bounded waits run out; bit 1 makes
+ * Test hooks, process-wide.  Bit 0 makes the load warp of the prefill kernels and
+ * of swa_hh_scores issue no copies, so that its consumers' bounded waits run out; bit 1 makes
  * swa_fwd / swa_fwd_varlen use the one-query-tile kernel even where another
  * kernel applies; bit 2 keeps them off the short-window stream kernel (d = 64,
  * window <= 129, no sinks), so the two-tile kernel runs instead.  For
