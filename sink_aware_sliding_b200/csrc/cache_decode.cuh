@@ -16,6 +16,7 @@
 
 #include <cstdint>
 
+#include "fixed_cache.h"
 #include "ptx.cuh"
 
 namespace swa {
@@ -186,12 +187,8 @@ __device__ __forceinline__ void merge_done(int c) {
   if (c > 1) cooperative_groups::this_cluster().barrier_wait();
 }
 
-// A decode kernel is launched while the kernel before it (the step's append, mostly) still
-// runs, and waits here for that kernel's end and its writes: the launch and the blocks'
-// start are out of the way by then.  The append kernels let it go at once.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// Launch with clusters of c blocks that may start early (see above).
+// Launch with clusters of c blocks that may start while the kernel before them (the step's append, mostly) ends;
+// they wait for it before they read anything.
 template <typename Kernel, typename Args>
 cudaError_t launch_decode_cluster(Kernel kernel, const Args& a, long long segments, int c, size_t smem,
                                   cudaStream_t stream) {

@@ -22,10 +22,27 @@ struct FastDiv {
 };
 
 #ifdef __CUDACC__
-// In a kernel that a decode follows: the decode's blocks may start (they wait for this
-// kernel's end before they read anything).
+// A kernel that is launched to start early (cudaLaunchAttributeProgrammaticStreamSerialization)
+// waits here for the end and the writes of the kernel before it: its launch and its blocks' start
+// are out of the way by then.  The kernels that such a one follows let it go at once.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 #endif
+
+// Launch of a kernel that starts early and waits, as above.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
 
 // Let a kernel use up to `bytes` of dynamic shared memory: asked of the runtime once per
 // device, since the question costs as much as a tenth of a launch.

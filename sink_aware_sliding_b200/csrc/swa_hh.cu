@@ -154,6 +154,7 @@ __global__ void __launch_bounds__(kFillThreads)
   __shared__ unsigned s_warp[kFillWarps];
   __shared__ unsigned s_cut, s_left;
   __shared__ int s_kept[kFillWarps], s_ties[kFillWarps];
+  let_next_kernel_start();  // the copy of the rows; the blocks here are fewer than the SMs where there is one
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* in = score_in + static_cast<size_t>(blockIdx.x) * L;
   int32_t* sp = slot_pos + static_cast<size_t>(blockIdx.x) * C;
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kFillThreads)
 __global__ void __launch_bounds__(256)
     swa_hh_gather_kernel(const __grid_constant__ FillRows rows, int L, const int32_t* __restrict__ slot_pos, int C,
                          int per) {
+  wait_for_previous_kernel();
   const size_t seg = blockIdx.x / per;
   copy_rows(rows, seg, L, C, slot_pos + seg * C, blockIdx.x % per * 256 + threadIdx.x, per * 256);
 }
@@ -342,8 +344,8 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
   if (e != cudaSuccess || kept == 0 || here) return e;
   const int blocks = (kept * vec + 255) / 256;
   const int per = std::min(blocks, std::max(1, (sms * 32 + segs - 1) / segs));
-  swa_hh_gather_kernel<<<static_cast<unsigned>(per) * segs, 256, 0, stream>>>(rows, L, slot_pos, C, per);
-  return cudaGetLastError();
+  return launch_early(swa_hh_gather_kernel, dim3(static_cast<unsigned>(per) * segs), 256, stream, rows, L, slot_pos, C,
+                      per);
 }
 
 }  // namespace swa

@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(256)
                         uint8_t* sk, uint8_t* sv, int B, FastDiv hkv, int W, int S) {
   constexpr int NG = D / kKv4Group;
   constexpr int ROW = kv4_row_bytes(D);
+  let_next_kernel_start();
   const int Hkv = static_cast<int>(hkv.d);
   const int n_ring = min(P, W), first = P - n_ring;
   const int n_old = min(min(P, S), first);  // sinks that have left the window
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(256)
                         const uint8_t* __restrict__ sv, void* k_out, void* v_out, int B, FastDiv hkv, FastDiv w, int S) {
   constexpr int NG = D / kKv4Group;
   constexpr int ROW = kv4_row_bytes(D);
+  wait_for_previous_kernel();
   const int Hkv = static_cast<int>(hkv.d), W = static_cast<int>(w.d);
   const uint8_t* ring = blockIdx.y ? vc : kc;
   const uint8_t* sink = blockIdx.y ? sv : sk;
@@ -291,15 +293,11 @@ cudaError_t launch_kv4_read(const int32_t* positions, int n, const void* kc, con
   const auto* c1 = static_cast<const uint8_t*>(vc);
   const auto* s0 = static_cast<const uint8_t*>(sk);
   const auto* s1 = static_cast<const uint8_t*>(sv);
-  if (d == 128 && f32)
-    swa_kv4_read_kernel<128, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
-  else if (d == 128)
-    swa_kv4_read_kernel<128, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
-  else if (f32)
-    swa_kv4_read_kernel<64, true><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
-  else
-    swa_kv4_read_kernel<64, false><<<grid, 256, 0, stream>>>(positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
-  return cudaGetLastError();
+  const auto launch = [&](auto kernel) {
+    return launch_early(kernel, grid, 256, stream, positions, n, c0, c1, s0, s1, k_out, v_out, B, hkv, w, S);
+  };
+  if (d == 128) return f32 ? launch(swa_kv4_read_kernel<128, true>) : launch(swa_kv4_read_kernel<128, false>);
+  return f32 ? launch(swa_kv4_read_kernel<64, true>) : launch(swa_kv4_read_kernel<64, false>);
 }
 
 }  // namespace swa
