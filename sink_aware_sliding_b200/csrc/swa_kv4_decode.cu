@@ -11,17 +11,19 @@
 // final scaling.  Steps are applied in fp32; minima times the sums of q, and times P, are
 // products as well, with the sums in three bf16 parts and P in two.  p a_j is the one value
 // that is rounded coarsely, to fp16 (2^-11): softmax numerators in 16 bits as in the
-// bf16 decode, with the running reference chosen so that p a_j stays below 2^15
-// whatever the steps are.
+// bf16 decode.  Two running references keep it in range: p and its sum are relative to the
+// logits' maximum alone, and O is in units of a power of two that follows V's largest step.
+// (One reference for both loses keys: with V = 0 in one tile and 1e15 in the next it moves by
+// 2^137, and the sum of p of the first tile with it.)
 //
 // Keys are the 16 rows of the products and up to eight query heads their columns: half the
 // products of the other orientation, and the codes go into the operand's registers as they
 // are masked; the scores are turned through shared memory (one 1 KB tile a warp) to become
 // an operand of P V.  Bound by instruction issue, masks and permutes above all (ALU pipe 57%,
 // issue 59% over a launch with its tail), next to HBM: 293 instructions per 16 keys and warp.
-// B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 66 us,
-// 5.1 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
-// 75 us with the keys as rows, 66 us with 32 keys a step.  Under a power cap that lowers the
+// B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 67.5 us,
+// 5.0 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
+// 75 us with the keys as rows, 66 us with 32 keys a step, 67.5 us with V's scale apart from p's.  Under a power cap that lowers the
 // clock to 1.7 GHz it takes 73 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,6 +42,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStages = 2;       // one tile is worked on while the next one comes: 80 KB in flight on an SM
 constexpr int kRows = 32;        // keys per tile: two products of 16 rows share a step of the softmax
 constexpr int kBlocksPerSm = 4;  // 16 warps: what 128 registers a thread allow
+// p <= 2^kSlack, and V's steps are below 2^(size + 1), so that p 2^(kTop - size) step < 2^15: fp16.
+constexpr int kSlack = 6, kTop = 8, kSizeMin = -90, kSizeMax = 110;
 
 template <int D>
 struct K4 {
@@ -78,6 +82,9 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[NW], const uint8_t* p) {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
 }
+
+// 2^x, exactly; -126 <= x <= 127.
+__device__ __forceinline__ float pow2(int x) { return __uint_as_float(static_cast<uint32_t>(x + 127) << 23); }
 
 // Exponent bits of a group's step, or of its |minimum| less 24 where that is more (a group
 // of one value), as those of a bf16.
@@ -202,7 +209,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   for (int j = 0; j < NG; ++j)
 #pragma unroll
     for (int x = 0; x < 2; ++x) o[j][x][0] = o[j][x][1] = o[j][x][2] = o[j][x][3] = 0.f;
-  float ref = -INFINITY, l = 0.f;
+  float ref = -INFINITY, l = 0.f;  // of head g: the logits' reference, and the sum of p = 2^(z - ref)
+  int size = kSizeMin;             // O and om are sums of p 2^(kTop - size) V
   // Scores: rows g and g + 8 of the product are the tokens kr and kr + 8; P and V: this
   // lane's tokens are 2t, 2t + 1 and those + 8.  In rows of 80 bytes both orders keep the
   // reads off each other's banks (K: two rows per quarter warp, V: four per half warp).
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
       for (int i = 0; i < 8; ++i)
         if (token(i) >= n) z[i] = -INFINITY;
     }
-    // ---- reference: p times the tile's largest step stays within fp16
+    // ---- references
     float mx = max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), fmaxf(z[6], z[7]));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
@@ -279,28 +287,33 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
       for (int j = 1; j < NG; ++j) big = max(big, size_of(w[j]));
     }
     big = __reduce_max_sync(kFull, big);
-    const int be = min(max((big >> 7) - 127, -90), 100);
-    // p a_j < 2^(8 + 1) at the reference, up to 2^15 before it is moved
-    const float want = mx + static_cast<float>(be - 8);
-    if (__any_sync(kFull, want > ref + 6.f)) {
-      const float next = want > ref + 6.f ? want : ref;
+    big = min(max((big >> 7) - 127, kSizeMin), kSizeMax);
+    if (__any_sync(kFull, mx > ref + static_cast<float>(kSlack)) || big > size) {
+      const float next = mx > ref + static_cast<float>(kSlack) ? mx : ref;
       const float alpha = ref == -INFINITY ? 0.f : ex2_approx(ref - next);
       const float a0 = __shfl_sync(kFull, alpha, 8 * t), a1 = __shfl_sync(kFull, alpha, 8 * t + 4);
+      const float down = big > size ? pow2(max(size - big, -126)) : 1.f;
       ref = next;
+      size = max(size, big);
       l *= alpha;
-      om[0] *= a0;
-      om[1] *= a1;
+      om[0] *= a0 * down;
+      om[1] *= a1 * down;
 #pragma unroll
       for (int j = 0; j < NG; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          o[j][x][0] *= a0; o[j][x][1] *= a1; o[j][x][2] *= a0; o[j][x][3] *= a1;
+          o[j][x][0] *= a0 * down; o[j][x][1] *= a1 * down; o[j][x][2] *= a0 * down; o[j][x][3] *= a1 * down;
         }
     }
     const float base = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = ex2_approx(z[i] - base);
     l += ((z[0] + z[1]) + (z[2] + z[3])) + ((z[4] + z[5]) + (z[6] + z[7]));
+    {
+      const float unit = pow2(kTop - size);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) f2_unpack(f2_mul(f2_pack(z[i], z[i + 1]), f2_pack(unit, unit)), z[i], z[i + 1]);
+    }
 
     // ---- O += P V, 16 tokens at a time
 #pragma unroll
@@ -347,28 +360,34 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   cp_async_wait<0>();
   __syncwarp();
 
-  // ---- this warp's state, in its own (now idle) stages
+  // ---- this warp's state, in its own (now idle) stages, relative to its own sum, so that the references
+  // of two warps differ by no more than their shares and large V stays finite: l in [2^-9, 2^-8)
   static_assert(2 * sizeof(Partial<D>) <= kStages * C::STAGE, "a warp's state and the block's fit a warp's stages");
   auto part = [&](int w) { return reinterpret_cast<Partial<D>*>(smem + w * C::WARP); };
   Partial<D>* pt = part(warp);
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
+  // without keys, or with a NaN or an infinity among them, as it is
+  const int shift = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 + 9 : 0;
+  const float fix = pow2(-shift), unit = pow2(size - kTop);
+  const float f0 = __shfl_sync(kFull, fix, 8 * t), f1 = __shfl_sync(kFull, fix, 8 * t + 4);
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
     const float m0 = __shfl_sync(kFull, om[0], 4 * j + t), m1 = __shfl_sync(kFull, om[1], 4 * j + t);
     constexpr float kEven = 16777216.f, kOdd = 1048576.f;  // 2^24, 2^20
+    auto value = [&](float x, float code, float m, float f) { return fmaf(x, code, m) * f * unit; };
     if (2 * t < G)
       *reinterpret_cast<float4*>(&pt->o[2 * t][32 * j + 4 * g]) =
-          make_float4(fmaf(o[j][0][0], kEven, m0), fmaf(o[j][1][0], kOdd, m0), fmaf(o[j][0][2], kEven, m0),
-                      fmaf(o[j][1][2], kOdd, m0));
+          make_float4(value(o[j][0][0], kEven, m0, f0), value(o[j][1][0], kOdd, m0, f0),
+                      value(o[j][0][2], kEven, m0, f0), value(o[j][1][2], kOdd, m0, f0));
     if (2 * t + 1 < G)
       *reinterpret_cast<float4*>(&pt->o[2 * t + 1][32 * j + 4 * g]) =
-          make_float4(fmaf(o[j][0][1], kEven, m1), fmaf(o[j][1][1], kOdd, m1), fmaf(o[j][0][3], kEven, m1),
-                      fmaf(o[j][1][3], kOdd, m1));
+          make_float4(value(o[j][0][1], kEven, m1, f1), value(o[j][1][1], kOdd, m1, f1),
+                      value(o[j][0][3], kEven, m1, f1), value(o[j][1][3], kOdd, m1, f1));
   }
   if (t == 0) {
-    pt->ref[g] = ref;
-    pt->l[g] = l;
+    pt->ref[g] = ref + static_cast<float>(shift);
+    pt->l[g] = l * fix;
   }
   merge_and_store<D>(part, part(0) + 1, s_lse2, G, c, rank, head0, a.out, a.out_f32 != 0, a.lse);
   merge_done(c);

@@ -364,3 +364,66 @@ def test_captured_behind_copies_and_a_join_of_streams():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want), f.__name__
+
+
+def check_parts(q, c, pos, kq, vq, coarse):
+    """Decode and compare with weights and terms of each element in 64 bits; kq, vq = (codes, steps, minima) of the slots'
+    rows, as kv4_quantise gives them.  `coarse`: relative error of a numerator times a step, of the largest such term of
+    the sequence (an array of each element's own allowance, or a number times the sums of its terms)."""
+    B, Hq, d = q.shape
+    H = vq[0].shape[1]
+    out, lse = torch.full((B, Hq, d), 7.0, device="cuda"), torch.full((B, Hq), 7.0, device="cuda")
+    swa.swa_kv4_decode(q.cuda(), *c.args(), torch.tensor(pos, dtype=torch.int32, device="cuda"), out, lse, c.W, c.S)
+    torch.cuda.synchronize()
+    got, gl, q64 = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().numpy()
+    for b in range(B):
+        n = min(int(pos[b]) + 1, c.W)
+        for h in range(Hq):
+            kv = h // (Hq // H)
+            kc, ks, kl = (x[b, kv, :n] for x in kq)
+            vc, vs, vl = (x[b, kv, :n] for x in vq)
+            k = kc * np.repeat(ks, 32, -1) + np.repeat(kl, 32, -1)
+            z = k @ q64[b, h] / math.sqrt(d)
+            w = np.exp(z - z.max())
+            total = w.sum()
+            w, wl = w / total, z.max() + np.log(total)
+            step, low = np.repeat(vs, 32, -1), np.repeat(vl, 32, -1)
+            want = w @ (vc * step + low)
+            # sums of the terms' sizes: minima carry two bf16 parts (2^-16), the products of a warp's 16 keys each are
+            # added up in float32 (2^-22 a step, n / 64 steps at least four warps apart, and the merge)
+            minima, codes = w @ np.abs(low), w @ (vc * step)
+            size = (np.abs(q64[b, h]) @ np.abs(k).T).max() / math.sqrt(d)
+            dz = size * ((d + 16) * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -20
+            tol = coarse(w, vs, codes) + 2.0 ** -16 * minima + (2 * dz + (n / 64 + 16) * 2.0 ** -22) * (minima + codes)
+            assert (np.abs(got[b, h] - want) <= tol + 1e-36).all(), (b, h, (np.abs(got[b, h] - want) - tol).max())
+            assert abs(gl[b, h] - wl) <= dz + 2.0 ** -22 * abs(wl) + 2.0 ** -18, (b, h, gl[b, h], wl)
+
+
+def eleven_bits(w, vs, codes):
+    """fp16 numerators with one reference for all groups: 2^-11 of the largest term."""
+    return 2.0 ** -11 * 15 * float(vs.max())
+
+
+def packed(k, v, W):
+    """A cache of these rows [B, H, W, d], and their codes, steps and minima."""
+    B, H, _, d = k.shape
+    c = Cache(B, H, d, W, 0)
+    c.kc.copy_(torch.from_numpy(oracle.kv4_pack(k)))
+    c.vc.copy_(torch.from_numpy(oracle.kv4_pack(v)))
+    return c, oracle.kv4_quantise(k), oracle.kv4_quantise(v)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,W", [(1, 64), (1, 128), (1, 256), (2, 4096), (150, 300)])
+@pytest.mark.parametrize("large", [1e12, 1e15, -1e25])
+def test_keys_without_values_count_beside_keys_of_large_ones(d, B, W, large):
+    """Half of the rows of V are zero, in front for one KV head and behind for the other, so that whole tiles, and with
+    few tiles whole warps, see nothing else; logits are near each other, so that every key has its share of the sum."""
+    H = 2
+    k, v = rand((B, H, W, d), 1, 0.05), rand((B, H, W, d), 2).float() * large
+    if large < 0:
+        v = torch.full((B, H, W, d), large)  # groups of one value: no steps
+    v[:, 0, :W // 2] = 0
+    v[:, 1, W // 2:] = 0
+    c, kq, vq = packed(k, v.bfloat16(), W)
+    check_parts(rand((B, 2 * H, d), 3), c, [W - 1] * B, kq, vq, eleven_bits)
