@@ -344,8 +344,11 @@ int swa_hadamard_proj(const void* y, const float* alpha, const float* beta, void
  * swa_kv4_decode: as swa_decode_ex (out_dtype SWA_DTYPE_BF16 or SWA_DTYPE_BF16_F32OUT)
  *   over the 4-bit cache.  It needs no workspace, so that any number of calls may run
  *   at once.  A sequence with pos[b] < 0 has no keys: out = 0, lse = -inf.  Scores and
- *   sums are float32; the softmax numerators, times a group's step, are rounded to 11
- *   significant bits.  Supported: Hq / Hkv <= 8, |q| < 2^100, step < 2^100.
+ *   sums are float32; the softmax numerators, and their products with the steps, are held
+ *   to 1.5 * 2^-17 (two bf16 parts), but for products below 2^-73 of the largest step or
+ *   minimum of the sequence's rows of V, which may lose bits.  Where a group of V is not
+ *   finite, only its own elements of the output are unspecified.
+ *   Supported: Hq / Hkv <= 8, |q| < 2^100, step < 2^100.
  */
 size_t swa_kv4_row_bytes(int d);
 int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* vcache, void* sink_k, void* sink_v,

@@ -4,27 +4,31 @@
 //   z_h = scale sum_j [ a_j (n_j . q_hj) + b_j sum(q_hj) ]
 //   O_h = sum_keys p_h [ a_j n_j + b_j ].
 // The integer part runs on the tensor cores with the codes as they are: a nibble in
-// the low bits of an fp16 word is the subnormal n 2^-24, one four bits higher is
-// 16 n 2^-24, so that "unpacking" is one AND per two elements and loses nothing.  q is
-// scaled by a power of two per head into fp16 (exact for all but elements 2^-28 below
-// the head's largest), and the odd nibbles' factor 16 goes into q and, for V, into the
-// final scaling.  Steps are applied in fp32; minima times the sums of q, and times P, are
-// products as well, with the sums in three bf16 parts and P in two.  p a_j is the one value
-// that is rounded coarsely, to fp16 (2^-11): softmax numerators in 16 bits as in the
-// bf16 decode.  Two running references keep it in range: p and its sum are relative to the
-// logits' maximum alone, and O is in units of a power of two that follows V's largest step.
-// (One reference for both loses keys: with V = 0 in one tile and 1e15 in the next it moves by
-// 2^137, and the sum of p of the first tile with it.)
+// the low bits of a 16-bit word is the subnormal n 2^-24 as fp16 (for K) and n 2^-133 as
+// bf16 (for V), one four bits higher is 16 times that, so that "unpacking" is one AND
+// per two elements and loses nothing.  q is scaled by a power of two per head into fp16
+// (exact for all but elements 2^-28 below the head's largest), and the odd nibbles' factor
+// 16 goes into q and, for V, into the final scaling.  K's steps are applied in fp32, its
+// minima times the sums of q are a product as well, with the sums in three bf16 parts.
+//
+// p and p a_j, which multiply V's minima and codes, are each the sum of two bf16 parts
+// (1.5 * 2^-17 together), which have the exponents of a float: a key or a group whose
+// p a_j is small next to another's keeps its bits down to 2^-73 of the largest step met.
+// (In one fp16 part, 11 bits, a group 2^33 below the largest of its tile came out as zeros;
+// 67.5 us against 69.3 us.)  Two running references: p and its sum are relative to
+// the logits' maximum alone, and O is in units of a power of two that follows V's largest
+// step.  (One reference for both loses keys: with V = 0 in one tile and 1e15 in the next it
+// moves by 2^137, and the sum of p of the first tile with it.)
 //
 // Keys are the 16 rows of the products and up to eight query heads their columns: half the
 // products of the other orientation, and the codes go into the operand's registers as they
 // are masked; the scores are turned through shared memory (one 1 KB tile a warp) to become
-// an operand of P V.  Bound by instruction issue, masks and permutes above all (ALU pipe 57%,
-// issue 59% over a launch with its tail), next to HBM: 293 instructions per 16 keys and warp.
-// B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 67.5 us,
-// 5.0 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
-// 75 us with the keys as rows, 66 us with 32 keys a step, 67.5 us with V's scale apart from p's.  Under a power cap that lowers the
-// clock to 1.7 GHz it takes 73 us.
+// an operand of P V.  Bound by instruction issue, masks and permutes above all (60% of the issue
+// slots and of the ALU pipe over a launch with its tail), next to HBM.
+// B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 69.3 us,
+// 4.8 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
+// 75 us with the keys as rows, 66 us with 32 keys a step and P in fp16.  Under a power cap that
+// lowers the clock to 1.76 GHz it takes 76 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -42,8 +46,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kStages = 2;       // one tile is worked on while the next one comes: 80 KB in flight on an SM
 constexpr int kRows = 32;        // keys per tile: two products of 16 rows share a step of the softmax
 constexpr int kBlocksPerSm = 4;  // 16 warps: what 128 registers a thread allow
-// p <= 2^kSlack, and V's steps are below 2^(size + 1), so that p 2^(kTop - size) step < 2^15: fp16.
-constexpr int kSlack = 6, kTop = 8, kSizeMin = -90, kSizeMax = 110;
+// p <= 2^kSlack, and V's steps and minima are below 2^(size + 1): their products with p 2^(kTop - size)
+// stay below 2^87, which leaves room for sums of 2^40 of them, and a code (2^-133) times a product
+// is a normal float as long as p step is above 2^-73 of 2^size.
+constexpr int kSlack = 6, kTop = 80, kSizeMin = -40;
 
 template <int D>
 struct K4 {
@@ -64,10 +70,30 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t pack_f16(uint64_t v) {
-  float lo, hi;
-  f2_unpack(v, lo, hi);
-  return pack_f16(lo, hi);
+// Two floats in two bf16 parts each: hi + lo is within 2^-17 of them.
+__device__ __forceinline__ void split_bf16(uint64_t v, uint32_t& hi, uint32_t& lo) {
+  float x, y;
+  f2_unpack(v, x, y);
+  hi = pack_bf16x2(x, y);
+  f2_unpack(f2_fma(f2_pack(step_of(hi), low_of(hi)), f2_pack(-1.f, -1.f), v), x, y);
+  lo = pack_bf16x2(x, y);
+}
+
+// Numerators (hi + lo) times steps in two bf16 parts again: the product of two 8-bit significands less its own
+// rounding fits 8 bits, so that only the last sum rounds, 2^-17 of the whole; together within 1.5 * 2^-17.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// minus_high: -round(hi * step), or with lo = 0 nothing, which gives the high part.
+__device__ __forceinline__ uint32_t low_times_step(uint32_t hi, uint32_t lo, uint32_t minus_high, uint32_t step) {
+  return fma_bf16x2(lo, step, fma_bf16x2(hi, step, minus_high));
 }
 
 template <int NW>
@@ -86,13 +112,16 @@ __device__ __forceinline__ void lds_words(uint32_t (&w)[NW], const uint8_t* p) {
 // 2^x, exactly; -126 <= x <= 127.
 __device__ __forceinline__ float pow2(int x) { return __uint_as_float(static_cast<uint32_t>(x + 127) << 23); }
 
-// Exponent bits of a group's step, or of its |minimum| less 24 where that is more (a group
-// of one value), as those of a bf16.
-__device__ __forceinline__ int size_of(uint32_t w) {
-  return max(static_cast<int>(w & 0x7fffu), static_cast<int>((w >> 16) & 0x7fffu) - (24 << 7));
+// The larger of `most` and of a group's step and |minimum|, in halves: a bf16's bits and 128, infinities and NaN
+// below all others (they are their own group's affair).
+__device__ __forceinline__ uint32_t larger(uint32_t w, uint32_t most) {
+  return __viaddmax_s16x2(w & 0x7fff7fffu, 0x00800080u, most);
 }
 
-template <int D>
+// FEW: up to four query heads a KV head.  P is the sum of two parts of bf16, and the low part of head h takes
+// column h + 4 of the product with V, which would be empty: as many products as P of one part takes.  With more
+// heads the low parts are products of their own (B = 64, 8 KV heads of 4: 69.3 us, and 75.3 us that way).
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
     swa_kv4_decode_kernel(const __grid_constant__ Kv4DecodeArgs a, int c) {
   using C = K4<D>;
@@ -209,7 +238,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   for (int j = 0; j < NG; ++j)
 #pragma unroll
     for (int x = 0; x < 2; ++x) o[j][x][0] = o[j][x][1] = o[j][x][2] = o[j][x][3] = 0.f;
-  float ref = -INFINITY, l = 0.f;  // of head g: the logits' reference, and the sum of p = 2^(z - ref)
+  float ref = -INFINITY, l = 0.f;  // of this lane's head: the logits' reference, and the sum of p = 2^(z - ref)
+  const int head = FEW ? g & 3 : g;
+  const uint32_t low_part = FEW && g >= 4 ? 0xffffffffu : 0u;
   int size = kSizeMin;             // O and om are sums of p 2^(kTop - size) V
   // Scores: rows g and g + 8 of the product are the tokens kr and kr + 8; P and V: this
   // lane's tokens are 2t, 2t + 1 and those + 8.  In rows of 80 bytes both orders keep the
@@ -262,11 +293,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
           make_float2(fmaf(z2, qscale0, low[2]), fmaf(z3, qscale1, low[3]));
     }
     __syncwarp();
-    // ---- turned: head g, tokens 2t, 2t + 1 and those + 8, 16, 24
+    // ---- turned: this lane's head, tokens 2t, 2t + 1 and those + 8, 16, 24
     float z[8];
     auto token = [&](int i) { return 2 * t + (i & 1) + (i >> 1) * 8; };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = scores[token(i) * kDecHeads + g];
+    for (int i = 0; i < 8; ++i) z[i] = scores[token(i) * kDecHeads + head];
     if (tile >= full_tiles) {
       const bool in_ring = tile < ring_tiles;
       const int n = (in_ring ? n_ring : n_sink) - (in_ring ? tile : tile - ring_tiles) * kRows;
@@ -280,19 +311,18 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
     int big;
     {
-      uint32_t w[NG];
+      uint32_t w[NG], most = 0u;
       lds_words<NG>(w, vt + lane * C::ROW + C::CODES);
-      big = size_of(w[0]);
 #pragma unroll
-      for (int j = 1; j < NG; ++j) big = max(big, size_of(w[j]));
+      for (int j = 0; j < NG; ++j) most = larger(w[j], most);
+      big = __reduce_max_sync(kFull, static_cast<int>(max(most & 0xffffu, most >> 16)));
     }
-    big = __reduce_max_sync(kFull, big);
-    big = min(max((big >> 7) - 127, kSizeMin), kSizeMax);
+    big = max((big >> 7) - 128, kSizeMin);
     if (__any_sync(kFull, mx > ref + static_cast<float>(kSlack)) || big > size) {
       const float next = mx > ref + static_cast<float>(kSlack) ? mx : ref;
       const float alpha = ref == -INFINITY ? 0.f : ex2_approx(ref - next);
       const float a0 = __shfl_sync(kFull, alpha, 8 * t), a1 = __shfl_sync(kFull, alpha, 8 * t + 4);
-      const float down = big > size ? pow2(max(size - big, -126)) : 1.f;
+      const float down = size - big < -126 ? 0.f : pow2(min(size - big, 0));
       ref = next;
       size = max(size, big);
       l *= alpha;
@@ -324,6 +354,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
       lds_words<NG>(p1, v0 + vpar + C::ROW);
       lds_words<NG>(p2, v0 + vpar + 8 * C::ROW);
       lds_words<NG>(p3, v0 + vpar + 9 * C::ROW);
+      uint32_t ph0, ph1, pl0, pl1;
+      split_bf16(f2_pack(z[4 * hf], z[4 * hf + 1]), ph0, pl0);
+      split_bf16(f2_pack(z[4 * hf + 2], z[4 * hf + 3]), ph1, pl1);
       {
         // the minima times P in two bf16 parts: row g of the product is group g % NG, and so is row g + 8
         const uint8_t* q = v0 + vpar + g % NG * 4;
@@ -331,28 +364,47 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
                                         *reinterpret_cast<const uint32_t*>(q + C::ROW), 0x7632);
         const uint32_t m1 = __byte_perm(*reinterpret_cast<const uint32_t*>(q + 8 * C::ROW),
                                         *reinterpret_cast<const uint32_t*>(q + 9 * C::ROW), 0x7632);
-        const uint32_t h0 = pack_bf16x2(z[4 * hf], z[4 * hf + 1]), h1 = pack_bf16x2(z[4 * hf + 2], z[4 * hf + 3]);
-        const uint32_t l0 = pack_bf16x2(z[4 * hf] - step_of(h0), z[4 * hf + 1] - low_of(h0));
-        const uint32_t l1 = pack_bf16x2(z[4 * hf + 2] - step_of(h1), z[4 * hf + 3] - low_of(h1));
-        mma_bf16_16816(om, m0, m0, m1, m1, h0, h1);
-        mma_bf16_16816(om, m0, m0, m1, m1, l0, l1);
+        if constexpr (FEW) {
+          mma_bf16_16816(om, m0, m0, m1, m1, low_part ? pl0 : ph0, low_part ? pl1 : ph1);
+        } else {
+          mma_bf16_16816(om, m0, m0, m1, m1, ph0, ph1);
+          mma_bf16_16816(om, m0, m0, m1, m1, pl0, pl1);
+        }
+      }
+      // FEW: this lane's column takes the high part less nothing, or the low part, which is less the high one
+      const uint32_t less0 = (ph0 ^ 0x80008000u) & low_part, less1 = (ph1 ^ 0x80008000u) & low_part;
+      if constexpr (FEW) {
+        pl0 &= low_part;
+        pl1 &= low_part;
       }
       uint32_t va[NG / 2], vb[NG / 2], vc[NG / 2], vd[NG / 2];
       lds_words<NG / 2>(va, v0 + vcode);
       lds_words<NG / 2>(vb, v0 + vcode + C::ROW);
       lds_words<NG / 2>(vc, v0 + vcode + 8 * C::ROW);
       lds_words<NG / 2>(vd, v0 + vcode + 9 * C::ROW);
-      const uint64_t pr0 = f2_pack(z[4 * hf], z[4 * hf + 1]), pr1 = f2_pack(z[4 * hf + 2], z[4 * hf + 3]);
-  #pragma unroll
+#pragma unroll
       for (int j = 0; j < NG; ++j) {
-        const uint32_t b0 = pack_f16(f2_mul(pr0, f2_pack(step_of(p0[j]), step_of(p1[j]))));
-        const uint32_t b1 = pack_f16(f2_mul(pr1, f2_pack(step_of(p2[j]), step_of(p3[j]))));
+        const uint32_t a0 = __byte_perm(p0[j], p1[j], 0x5410), a1 = __byte_perm(p2[j], p3[j], 0x5410);
         // elements 4 g + i of group j: tokens 2t (low half) and 2t + 1
         const uint32_t x = __byte_perm(va[j >> 1], vb[j >> 1], (j & 1) ? 0x7632 : 0x5410);
         const uint32_t y = __byte_perm(vc[j >> 1], vd[j >> 1], (j & 1) ? 0x7632 : 0x5410);
         const uint32_t xh = x >> 8, yh = y >> 8;
-        mma_f16_16816(o[j][0], x & 0x000f000fu, xh & 0x000f000fu, y & 0x000f000fu, yh & 0x000f000fu, b0, b1);
-        mma_f16_16816(o[j][1], x & 0x00f000f0u, xh & 0x00f000f0u, y & 0x00f000f0u, yh & 0x00f000f0u, b0, b1);
+        const uint32_t e0 = x & 0x000f000fu, e1 = xh & 0x000f000fu, e2 = y & 0x000f000fu, e3 = yh & 0x000f000fu;
+        const uint32_t d0 = x & 0x00f000f0u, d1 = xh & 0x00f000f0u, d2 = y & 0x00f000f0u, d3 = yh & 0x00f000f0u;
+        if constexpr (FEW) {
+          const uint32_t b0 = low_times_step(ph0, pl0, mul_bf16x2(less0, a0), a0);
+          const uint32_t b1 = low_times_step(ph1, pl1, mul_bf16x2(less1, a1), a1);
+          mma_bf16_16816(o[j][0], e0, e1, e2, e3, b0, b1);
+          mma_bf16_16816(o[j][1], d0, d1, d2, d3, b0, b1);
+        } else {
+          const uint32_t h0 = mul_bf16x2(ph0, a0), h1 = mul_bf16x2(ph1, a1);
+          const uint32_t l0 = low_times_step(ph0, pl0, h0 ^ 0x80008000u, a0);
+          const uint32_t l1 = low_times_step(ph1, pl1, h1 ^ 0x80008000u, a1);
+          mma_bf16_16816(o[j][0], e0, e1, e2, e3, h0, h1);
+          mma_bf16_16816(o[j][1], d0, d1, d2, d3, h0, h1);
+          mma_bf16_16816(o[j][0], e0, e1, e2, e3, l0, l1);
+          mma_bf16_16816(o[j][1], d0, d1, d2, d3, l0, l1);
+        }
       }
     }
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -367,15 +419,26 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   Partial<D>* pt = part(warp);
   l += __shfl_xor_sync(kFull, l, 1);
   l += __shfl_xor_sync(kFull, l, 2);
+  if constexpr (FEW) {  // high and low parts
+#pragma unroll
+    for (int i = 0; i < 2; ++i) om[i] += __shfl_xor_sync(kFull, om[i], 2);
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][x][i] += __shfl_xor_sync(kFull, o[j][x][i], 2);
+  }
   // without keys, or with a NaN or an infinity among them, as it is
   const int shift = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 + 9 : 0;
-  const float fix = pow2(-shift), unit = pow2(size - kTop);
+  constexpr int kDown = 64;  // on the way, so that no factor leaves the range of a float
+  const float fix = pow2(-shift), unit = pow2(size - kTop + kDown);
   const float f0 = __shfl_sync(kFull, fix, 8 * t), f1 = __shfl_sync(kFull, fix, 8 * t + 4);
 #pragma unroll
   for (int j = 0; j < NG; ++j) {
     const float m0 = __shfl_sync(kFull, om[0], 4 * j + t), m1 = __shfl_sync(kFull, om[1], 4 * j + t);
-    constexpr float kEven = 16777216.f, kOdd = 1048576.f;  // 2^24, 2^20
-    auto value = [&](float x, float code, float m, float f) { return fmaf(x, code, m) * f * unit; };
+    const float kEven = pow2(133 - kDown), kOdd = pow2(129 - kDown);
+    auto value = [&](float x, float code, float m, float f) { return fmaf(x, code, m * pow2(-kDown)) * f * unit; };
     if (2 * t < G)
       *reinterpret_cast<float4*>(&pt->o[2 * t][32 * j + 4 * g]) =
           make_float4(value(o[j][0][0], kEven, m0, f0), value(o[j][1][0], kOdd, m0, f0),
@@ -393,24 +456,25 @@ __global__ void __launch_bounds__(kDecWarps * 32, kBlocksPerSm)
   merge_done(c);
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_impl(const Kv4DecodeArgs& a, int sms, cudaStream_t stream) {
   const size_t smem = kDecWarps * K4<D>::WARP;
   const long long segments = static_cast<long long>(a.B) * a.Hkv;
   const long long tiles = (static_cast<long long>(a.W) + a.S + kRows - 1) / kRows;
-  // 512 segments: 73 us with one block each (3.5 on an SM: some have 4), 66 us with two, 84 us with four, whose
-  // starts and merges weigh more
+  // 512 segments, with P in fp16: 73 us with one block each (3.5 on an SM: some have 4), 66 us with two, 84 us with
+  // four, whose starts and merges weigh more
   const int c = decode_cluster(segments, tiles, sms, kBlocksPerSm, 1);
   if (segments * c > INT32_MAX) return cudaErrorInvalidValue;
-  cudaError_t e = allow_shared<swa_kv4_decode_kernel<D>>(static_cast<int>(smem));
+  cudaError_t e = allow_shared<swa_kv4_decode_kernel<D, FEW>>(static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_decode_cluster(swa_kv4_decode_kernel<D>, a, segments, c, smem, stream);
+  return launch_decode_cluster(swa_kv4_decode_kernel<D, FEW>, a, segments, c, smem, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_decode(const Kv4DecodeArgs& a, int d, int sms, cudaStream_t stream) {
-  return d == 128 ? launch_impl<128>(a, sms, stream) : launch_impl<64>(a, sms, stream);
+  if (a.G <= 4) return d == 128 ? launch_impl<128, true>(a, sms, stream) : launch_impl<64, true>(a, sms, stream);
+  return d == 128 ? launch_impl<128, false>(a, sms, stream) : launch_impl<64, false>(a, sms, stream);
 }
 
 }  // namespace swa

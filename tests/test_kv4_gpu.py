@@ -368,8 +368,8 @@ def test_captured_behind_copies_and_a_join_of_streams():
 
 def check_parts(q, c, pos, kq, vq, coarse):
     """Decode and compare with weights and terms of each element in 64 bits; kq, vq = (codes, steps, minima) of the slots'
-    rows, as kv4_quantise gives them.  `coarse`: relative error of a numerator times a step, of the largest such term of
-    the sequence (an array of each element's own allowance, or a number times the sums of its terms)."""
+    rows, as kv4_quantise gives them.  coarse(weights, steps, sums of the code terms) is what the rounding of numerators times
+    steps may move each element by."""
     B, Hq, d = q.shape
     H = vq[0].shape[1]
     out, lse = torch.full((B, Hq, d), 7.0, device="cuda"), torch.full((B, Hq), 7.0, device="cuda")
@@ -427,3 +427,73 @@ def test_keys_without_values_count_beside_keys_of_large_ones(d, B, W, large):
     v[:, 1, W // 2:] = 0
     c, kq, vq = packed(k, v.bfloat16(), W)
     check_parts(rand((B, 2 * H, d), 3), c, [W - 1] * B, kq, vq, eleven_bits)
+
+
+def sixteen_bits(w, vs, codes):
+    """Numerators in two bf16 parts (2^-18) times steps in two again (2^-17): of each term, wherever the largest is."""
+    return 1.5 * 2.0 ** -17 * codes
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,W", [(1, 40), (2, 700), (150, 130)])
+@pytest.mark.parametrize("power", [-20, 0, 16, 20, 30, 40])
+def test_groups_of_small_steps_beside_one_of_large_ones(d, B, W, power):
+    """One group of V lies 2^power above the others, under a peaked softmax: every group keeps its own bits."""
+    H = 2
+    k, v = rand((B, H, W, d), 1), rand((B, H, W, d), 2).float()
+    v[..., 32:64] *= 2.0 ** power
+    c, kq, vq = packed(k, v.bfloat16(), W)
+    check_parts(rand((B, 4 * H, d), 3, 3.0), c, [W - 1] * B, kq, vq, sixteen_bits)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("W", [32, 200, 3000])
+@pytest.mark.parametrize("at", [0, -1])
+def test_a_large_value_of_negligible_weight_takes_no_bits_from_the_others(d, W, at):
+    """One key, in front or behind, with V 2^40 above the others and a weight of about 2^-40 or 2^-60 of theirs."""
+    B, H, G = 2, 2, 4
+    side = torch.sign(rand((H, 1, d), 5).float())
+    k, v = rand((B, H, W, d), 1, 0.1).float(), rand((B, H, W, d), 2).float()
+    power = torch.tensor([40.0, 60.0]).view(1, H, 1)
+    k[:, :, at] = (-side * power[..., None] * math.log(2) / math.sqrt(d)).squeeze(2)
+    v[:, :, at] *= 2.0 ** 40
+    q = (side + 0.1 * rand((B, H, G, d), 3).float()).flatten(1, 2).bfloat16()
+    c, kq, vq = packed(k.bfloat16(), v.bfloat16(), W)
+    check_parts(q, c, [W - 1] * B, kq, vq, sixteen_bits)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1e-27, 1e-12, 1e12, 1e27])
+def test_values_of_any_size_keep_sixteen_bits(d, scale):
+    B, H, W = 2, 2, 500
+    c, kq, vq = packed(rand((B, H, W, d), 1), (rand((B, H, W, d), 2).float() * scale).bfloat16(), W)
+    check_parts(rand((B, 4 * H, d), 3), c, [W - 1, 77], kq, vq, sixteen_bits)
+
+
+def test_constant_rows_next_to_the_largest_that_fill_takes():
+    """Values of 2^126: sums over keys, warps and blocks stay finite."""
+    for B, W in ((1, 4096), (150, 100)):
+        H, d = 2, 64
+        v = torch.full((B, H, W, d), 2.0 ** 126)
+        v[:, 1] *= -1
+        c, kq, vq = packed(rand((B, H, W, d), 1, 0.1), v.bfloat16(), W)
+        check_parts(rand((B, 2 * H, d), 3), c, [W - 1] * B, kq, vq, sixteen_bits)
+
+
+def test_a_group_that_is_not_finite_keeps_to_itself():
+    """Infinite or NaN parameters in one group of V: the other groups come out as without them, to the last bits."""
+    B, H, Hq, d, W = 1, 2, 8, 128, 300
+    k, v = rand((B, H, W, d), 1), rand((B, H, W, d), 2)
+    q, pos = rand((B, Hq, d), 3).cuda(), torch.full((B,), W - 1, dtype=torch.int32, device="cuda")
+    outs = []
+    for word in (None, [0x80, 0x7f, 0x80, 0xff], [0xc0, 0x7f, 0xc0, 0x7f]):
+        c, _, _ = packed(k, v, W)
+        if word:
+            c.vc[:, :, 40, d // 2 + 4:d // 2 + 8] = torch.tensor(word, dtype=torch.uint8, device="cuda")
+        outs.append(torch.empty(B, Hq, d, device="cuda"))
+        swa.swa_kv4_decode(q, *c.args(), pos, outs[-1], None, W, 0)
+    torch.cuda.synchronize()
+    rest = torch.arange(d) // 32 != 1
+    for out in outs[1:]:
+        assert not torch.isfinite(out[..., 32:64]).any()
+        assert float((out - outs[0])[..., rest].abs().max()) <= 2.0 ** -20 * float(outs[0].abs().max())
