@@ -25,6 +25,8 @@ struct FastDiv {
 // A kernel that is launched to start early (cudaLaunchAttributeProgrammaticStreamSerialization)
 // waits here for the end and the writes of the kernel before it: its launch and its blocks' start
 // are out of the way by then.  The kernels that such a one follows let it go at once.
+// What the kernel before may write is no `const __restrict__` parameter of the early one: that
+// would promise memory that nobody writes while it runs, and allow loads that are not coherent.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 #endif

@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kFillThreads)
 
 // Copy the chosen rows, one thread per 16 bytes, `per` blocks a (b, KV head).
 __global__ void __launch_bounds__(256)
-    swa_hh_gather_kernel(const __grid_constant__ FillRows rows, int L, const int32_t* __restrict__ slot_pos, int C,
+    swa_hh_gather_kernel(const __grid_constant__ FillRows rows, int L, const int32_t* slot_pos, int C,
                          int per) {
   wait_for_previous_kernel();
   const size_t seg = blockIdx.x / per;

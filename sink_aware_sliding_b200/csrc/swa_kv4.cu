@@ -184,9 +184,8 @@ __global__ void __launch_bounds__(128)
 // Eight lanes a row, four elements of every group each.  blockIdx.y: 0 for k, 1 for v; blockIdx.z: the sequence.
 template <int D, bool F32>
 __global__ void __launch_bounds__(256)
-    swa_kv4_read_kernel(const int32_t* __restrict__ positions, int n, const uint8_t* __restrict__ kc,
-                        const uint8_t* __restrict__ vc, const uint8_t* __restrict__ sk,
-                        const uint8_t* __restrict__ sv, void* k_out, void* v_out, int B, FastDiv hkv, FastDiv w, int S) {
+    swa_kv4_read_kernel(const int32_t* positions, int n, const uint8_t* kc, const uint8_t* vc, const uint8_t* sk,
+                        const uint8_t* sv, void* k_out, void* v_out, int B, FastDiv hkv, FastDiv w, int S) {
   constexpr int NG = D / kKv4Group;
   constexpr int ROW = kv4_row_bytes(D);
   wait_for_previous_kernel();

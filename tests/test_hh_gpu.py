@@ -372,3 +372,34 @@ def test_calls_on_a_stream_given_by_hand_and_without_sequences():
     swa.swa_hh_cache_append(k[:0, :, 0].contiguous().cuda(), v[:0, :, 0].contiguous().cuda(),
                             torch.zeros(0, dtype=torch.int32, device="cuda"), *none, None, 0, 1)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("C,d", [(1001, 128), (2045, 64)])
+def test_fills_of_the_same_cache_one_after_another(C, d):
+    """Capacities whose heads share sectors of slot_pos, filled again and again in place with other prompts, eagerly and
+    in a graph: the copying kernel, which starts while the choice is still being written, takes the new positions."""
+    B, H, L, S, recent = 4, 8, 5000, 3, 200
+    sets = []
+    for seed in range(3):
+        k, s = rand((B, L, H, d), seed).cuda(), torch.rand(B, H, L, generator=torch.Generator().manual_seed(seed)).cuda()
+        always = (torch.arange(L, device="cuda") < S) | (torch.arange(L, device="cuda") >= L - recent)
+        keep = s.masked_fill(always, 2.0).sort(dim=-1, descending=True, stable=True)[1][..., :C].sort(-1)[0]
+        at = keep.transpose(1, 2)[..., None].expand(-1, -1, -1, d)
+        sets.append((k, -k, s, keep.int(), k.gather(1, at).transpose(1, 2)))
+    kc, vc = (torch.zeros(B, H, C, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sp = torch.full((B, H, C), L - 1, device="cuda", dtype=torch.int32)  # valid, and wrong
+    score = torch.zeros(B, H, C, device="cuda")
+    k, v, s = (torch.empty_like(x) for x in sets[0][:3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        swa.swa_hh_cache_fill(k, v, s, kc, vc, sp, score, S, recent)
+    for n in range(12):
+        kn, vn, sn, keep, rows = sets[n % 3]
+        if n % 2:
+            for x, y in zip((k, v, s), (kn, vn, sn)):
+                x.copy_(y)
+            graph.replay()
+        else:
+            swa.swa_hh_cache_fill(kn, vn, sn, kc, vc, sp, score, S, recent)
+        assert torch.equal(sp, keep), n
+        assert torch.equal(kc, rows) and torch.equal(vc, -rows), n

@@ -497,3 +497,35 @@ def test_a_group_that_is_not_finite_keeps_to_itself():
     for out in outs[1:]:
         assert not torch.isfinite(out[..., 32:64]).any()
         assert float((out - outs[0])[..., rest].abs().max()) <= 2.0 ** -20 * float(outs[0].abs().max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_reads_behind_fills_of_the_same_cache(d):
+    """Filled again and again in place with other prompts and read at once, eagerly and in a graph: the read, which starts
+    while the fill still writes, takes the new rows, and the new positions of a copy."""
+    B, P, H, W, S = 4, 3001, 3, 2500, 5
+    c = Cache(B, H, d, W, S)
+    first = torch.arange(P - W, P, dtype=torch.int32).expand(B, -1).contiguous().cuda()
+    asks = [first, first.flip(1).contiguous()]
+    prompts = [rand((B, P, H, d), n).cuda() for n in range(3)]
+    want = [torch.from_numpy(oracle.kv4_values(x.cpu())).float().cuda()[:, P - W:] for x in prompts]
+    k, ask = torch.empty_like(prompts[0]), torch.empty_like(first)
+    ko, vo = (torch.zeros(B, W, H, d, device="cuda") for _ in range(2))
+
+    def both(x, at):
+        swa.swa_kv4_cache_fill(x, x, *c.args(), W, S)
+        swa.swa_kv4_cache_read(at, *c.args(), ko, vo, W, S)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(k, ask)
+    for n in range(12):
+        x, at = prompts[n % 3], asks[n // 2 % 2]
+        if n % 2:
+            k.copy_(x)
+            ask.copy_(at)
+            graph.replay()
+        else:
+            both(x, at)
+        w = want[n % 3] if n // 2 % 2 == 0 else want[n % 3].flip(1)
+        assert torch.equal(ko, w) and torch.equal(vo, w), n
