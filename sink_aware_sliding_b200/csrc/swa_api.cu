@@ -220,10 +220,15 @@ int swa_fwd_varlen(const void* q, const void* k, const void* v, void* out, float
                      dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
+static int check_cache_shape(int B, int Hkv, int d, int window, int n_sink) {
+  if (B < 0 || Hkv <= 0 || window < 1 || n_sink < 0) return SWA_ERR_INVALID_ARG;
+  return d == 64 || d == 128 ? SWA_OK : SWA_ERR_UNSUPPORTED;
+}
+
 static int check_cache(int B, int Hkv, int d, int window, int n_sink, const void* kc,
                        const void* vc, const void* sk, const void* sv) {
-  if (B < 0 || Hkv <= 0 || window < 1 || n_sink < 0) return SWA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return SWA_ERR_UNSUPPORTED;
+  const int st = check_cache_shape(B, Hkv, d, window, n_sink);
+  if (st != SWA_OK) return st;
   if (!kc || !vc || !aligned16(kc) || !aligned16(vc)) return SWA_ERR_INVALID_ARG;
   if (n_sink > 0 && (!sk || !sv || !aligned16(sk) || !aligned16(sv))) return SWA_ERR_INVALID_ARG;
   return SWA_OK;
@@ -542,11 +547,18 @@ int swa_based_linear_decode(const void* q, const void* k, const void* v, float* 
   return e == cudaSuccess ? SWA_OK : SWA_ERR_CUDA;
 }
 
+// An empty batch needs no cache: tensors without elements have no address.
+static int check_kv4(int B, int Hkv, int d, int window, int n_sink, const void* kc, const void* vc, const void* sk,
+                     const void* sv) {
+  return B == 0 ? check_cache_shape(B, Hkv, d, window, n_sink)
+                : check_cache(B, Hkv, d, window, n_sink, kc, vc, sk, sv);
+}
+
 size_t swa_kv4_row_bytes(int d) { return d == 64 || d == 128 ? swa::kv4_row_bytes(d) : 0; }
 
 int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* vcache, void* sink_k, void* sink_v,
                        int B, int Hkv, int d, int window, int n_sink, swa_stream_t stream) {
-  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  int st = check_kv4(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
   if (st != SWA_OK) return st;
   if (P < 0) return SWA_ERR_INVALID_ARG;
   if (P == 0 || B == 0) return SWA_OK;
@@ -563,7 +575,7 @@ int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* 
 int swa_kv4_cache_append(const void* k_new, const void* v_new, const int32_t* pos, void* kcache, void* vcache,
                          void* sink_k, void* sink_v, int B, int Hkv, int d, int window, int n_sink,
                          swa_stream_t stream) {
-  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  int st = check_kv4(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
   if (st != SWA_OK) return st;
   if (B == 0) return SWA_OK;
   if (static_cast<long long>(B) * Hkv > INT32_MAX) return SWA_ERR_UNSUPPORTED;
@@ -576,7 +588,7 @@ int swa_kv4_cache_append(const void* k_new, const void* v_new, const int32_t* po
 int swa_kv4_cache_read(const int32_t* positions, int n, const void* kcache, const void* vcache, const void* sink_k,
                        const void* sink_v, void* k_out, void* v_out, int out_dtype, int B, int Hkv, int d, int window,
                        int n_sink, swa_stream_t stream) {
-  int st = check_cache(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
+  int st = check_kv4(B, Hkv, d, window, n_sink, kcache, vcache, sink_k, sink_v);
   if (st != SWA_OK) return st;
   if (n < 0 || (out_dtype != SWA_DTYPE_BF16 && out_dtype != SWA_DTYPE_F32)) return SWA_ERR_INVALID_ARG;
   if (n == 0 || B == 0) return SWA_OK;

@@ -120,6 +120,21 @@ def test_rope_axes(lib, kw, want):
                                 len(a["sec"]), a["layout"], a["base"], a["inv"], a["dt"], None) == want
 
 
+@pytest.mark.parametrize("sinks", [0, 2])
+def test_an_empty_batch_of_the_4bit_cache_has_nothing_to_do(lib, sinks):
+    """Tensors without elements have no address; wrong sizes are refused all the same."""
+    none = dict(B=0, S=sinks, k=None, v=None, kc=None, vc=None, sk=None, sv=None, pos=None, q=None, out=None)
+    for name, order in (("swa_kv4_cache_fill", "k v P kc vc sk sv B Hkv d W S stream"),
+                        ("swa_kv4_cache_append", "k v pos kc vc sk sv B Hkv d W S stream"),
+                        ("swa_kv4_cache_read", "pos n kc vc sk sv out out dt B Hkv d W S stream"),
+                        ("swa_kv4_decode", "q kc vc sk sv pos out lse B Hq Hkv d W S scale dt stream")):
+        assert call(lib, name, order, KV4, **none) == OK
+        for wrong, want in ((dict(W=0), BAD), (dict(S=-1), BAD), (dict(Hkv=0), BAD), (dict(d=96), UNSUP)):
+            assert call(lib, name, order, KV4, **dict(none, **wrong)) == want
+    assert call(lib, "swa_kv4_cache_fill", "k v P kc vc sk sv B Hkv d W S stream", KV4, **dict(none, P=-1)) == BAD
+    assert call(lib, "swa_kv4_cache_read", "pos n kc vc sk sv out out dt B Hkv d W S stream", KV4, **dict(none, n=-1)) == BAD
+
+
 def test_binding_refuses_tensors_that_are_not_on_the_gpu(lib):
     t = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
     u = torch.zeros(1, 2, 8, 80, dtype=torch.uint8)

@@ -529,3 +529,15 @@ def test_reads_behind_fills_of_the_same_cache(d):
             both(x, at)
         w = want[n % 3] if n // 2 % 2 == 0 else want[n % 3].flip(1)
         assert torch.equal(ko, w) and torch.equal(vo, w), n
+
+
+@pytest.mark.parametrize("S", [0, 3])
+def test_calls_without_sequences(S):
+    c = Cache(2, 2, 64, 9, S)
+    none = [t[:0] for t in c.args()] if S else [c.kc[:0], c.vc[:0], None, None]
+    k, pos = rand((2, 4, 2, 64), 1).cuda(), torch.zeros(2, device="cuda", dtype=torch.int32)
+    swa.swa_kv4_cache_fill(k[:0], k[:0], *none, 9, S)
+    swa.swa_kv4_cache_append(k[:0, 0], k[:0, 0], pos[:0], *none, 9, S)
+    swa.swa_kv4_cache_read(pos[:0, None], *none, k[:0, :1], k[:0, :1], 9, S)
+    swa.swa_kv4_decode(k[:0, 0], *none, pos[:0], k[:0, 0], None, 9, S)
+    torch.cuda.synchronize()
