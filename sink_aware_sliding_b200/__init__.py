@@ -409,7 +409,7 @@ def _device(t, name: str) -> int:
 
 def _at(t, name: str, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of this type, shape and device."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {list(shape)} on the current CUDA device")
     return t.data_ptr()
 

@@ -541,3 +541,19 @@ def test_calls_without_sequences(S):
     swa.swa_kv4_cache_read(pos[:0, None], *none, k[:0, :1], k[:0, :1], 9, S)
     swa.swa_kv4_decode(k[:0, 0], *none, pos[:0], k[:0, 0], None, 9, S)
     torch.cuda.synchronize()
+
+
+def test_missing_tensors_are_refused_by_name():
+    c = Cache(1, 2, 64, 9, 3)
+    k, pos = rand((1, 2, 64), 1).cuda(), torch.zeros(1, device="cuda", dtype=torch.int32)
+    for sinks in ((None, None), (c.sk, None), (None, c.sv)):
+        for f in (lambda: swa.swa_kv4_cache_fill(k[None], k[None], c.kc, c.vc, *sinks, 9, 3),
+                  lambda: swa.swa_kv4_cache_append(k, k, pos, c.kc, c.vc, *sinks, 9, 3),
+                  lambda: swa.swa_kv4_cache_read(pos[None], c.kc, c.vc, *sinks, k[None], k[None], 9, 3),
+                  lambda: swa.swa_kv4_decode(k, c.kc, c.vc, *sinks, pos, k, None, 9, 3)):
+            with pytest.raises(ValueError, match="sink_k" if sinks[0] is None else "sink_v"):
+                f()
+    with pytest.raises(ValueError, match="pos"):
+        swa.swa_kv4_cache_append(k, k, None, c.kc, c.vc, c.sk, c.sv, 9, 3)
+    with pytest.raises(ValueError, match="v_new"):
+        swa.swa_kv4_cache_append(k, None, pos, c.kc, c.vc, c.sk, c.sv, 9, 3)
