@@ -414,6 +414,14 @@ def _at(t, name: str, dtype, shape, dev: int) -> int:
     return t.data_ptr()
 
 
+def _int(x, name: str) -> int:
+    """x as the C interface's 32-bit integer; ctypes would drop the upper bits."""
+    n = int(x)
+    if not -2 ** 31 <= n < 2 ** 31:
+        raise ValueError(f"{name}: an integer of 32 bits")
+    return n
+
+
 def _on(stream, dev: int):
     return _torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
@@ -423,6 +431,7 @@ def _kv4_cache(dev, kcache, vcache, sink_k, sink_v, B, Hkv, d, window, n_sink):
     row = d // 2 + d // 8
     ring = (B, Hkv, window, row)
     if n_sink <= 0:
+        _int(n_sink, "n_sink")  # window, and n_sink above 0, are sizes of tensors
         return _at(kcache, "kcache", u8, ring, dev), _at(vcache, "vcache", u8, ring, dev), None, None
     sink = (B, Hkv, n_sink, row)
     return (_at(kcache, "kcache", u8, ring, dev), _at(vcache, "vcache", u8, ring, dev),
@@ -510,8 +519,9 @@ def swa_hh_scores(q, k, lse, score, n_obs: int, window: int, n_sink: int, scale=
     Hkv = k.shape[2]
     st = _load().swa_hh_scores(_at(q, "q", _torch.bfloat16, q.shape, dev), _at(k, "k", _torch.bfloat16, (B, L, Hkv, d), dev),
                                _at(lse, "lse", _torch.float32, (B, Hq, L), dev),
-                               _at(score, "score", _torch.float32, (B, Hkv, L), dev), B, Hq, Hkv, L, d, int(n_obs),
-                               int(window), int(n_sink), _scale(scale, d), _on(stream, dev))
+                               _at(score, "score", _torch.float32, (B, Hkv, L), dev), B, Hq, Hkv, L, d,
+                               _int(n_obs, "n_obs"), min(int(window), max(L, 1)), _int(n_sink, "n_sink"),
+                               _scale(scale, d), _on(stream, dev))
     if st:
         _check(st, "swa_hh_scores")
 
@@ -533,7 +543,7 @@ def swa_hh_cache_fill(k, v, score_in, kcache, vcache, slot_pos, score, n_sink: i
     C, cache = _hh_cache(dev, kcache, vcache, slot_pos, score, B, Hkv, d)
     st = _load().swa_hh_cache_fill(_at(k, "k", _torch.bfloat16, shape, dev), _at(v, "v", _torch.bfloat16, shape, dev),
                                    _at(score_in, "score_in", _torch.float32, (B, Hkv, L), dev), L, *cache, B, Hkv, d, C,
-                                   int(n_sink), int(recent), _on(stream, dev))
+                                   _int(n_sink, "n_sink"), _int(recent, "recent"), _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_fill")
 
@@ -549,7 +559,7 @@ def swa_hh_cache_append(k_new, v_new, pos, kcache, vcache, slot_pos, score, slot
     st = _load().swa_hh_cache_append(_at(k_new, "k_new", _torch.bfloat16, shape, dev),
                                      _at(v_new, "v_new", _torch.bfloat16, shape, dev), _at(pos, "pos", _torch.int32, (B,), dev),
                                      *cache, None if slot is None else _at(slot, "slot", _torch.int32, (B, Hkv), dev), B, Hkv,
-                                     d, C, int(n_sink), int(recent), _on(stream, dev))
+                                     d, C, _int(n_sink, "n_sink"), _int(recent, "recent"), _on(stream, dev))
     if st:
         _check(st, "swa_hh_cache_append")
 
@@ -595,7 +605,7 @@ def swa_rope_axes_qk(q, k, positions, sections, layout: str = "sections", rope_b
         kp, Hkv, ks = _rope_rows(k, "k", T, d, dev)
     n_axes = len(sections)
     pp = _at(positions, "positions", _torch.int32, (n_axes, T), dev)
-    sec = (ctypes.c_int32 * max(1, n_axes))(*sections)
+    sec = (ctypes.c_int32 * max(1, n_axes))(*[_int(x, "sections") for x in sections])
     st = _load().swa_rope_axes_qk(qp, kp, pp, T, Hq, Hkv, d, qs, ks, sec, n_axes, _ROPE_LAYOUTS[layout],
                                   float(rope_base), 1 if inverse else 0,
                                   SWA_DTYPE_F32 if q.dtype is _torch.float32 else SWA_DTYPE_BF16, _on(stream, dev))

@@ -403,3 +403,27 @@ def test_fills_of_the_same_cache_one_after_another(C, d):
             swa.swa_hh_cache_fill(kn, vn, sn, kc, vc, sp, score, S, recent)
         assert torch.equal(sp, keep), n
         assert torch.equal(kc, rows) and torch.equal(vc, -rows), n
+
+
+def test_integers_that_do_not_fit_32_bits_are_refused():
+    """ctypes would drop their upper bits: 2^32 + 1 would be 1.  A window of any size from L on means all keys."""
+    k, v, sp, s = (t.cuda() for t in map(torch.as_tensor, cache(1, 2, 8, 64, 3, 1.0)))
+    x, lse, big = rand((1, 4, 2, 64), 4).cuda(), torch.zeros(1, 2, 4, device="cuda"), 2 ** 32
+    pos = torch.zeros(1, device="cuda", dtype=torch.int32)
+    for f in (lambda: swa.swa_hh_scores(x, x, lse, lse.clone(), big + 1, 4, 0),
+              lambda: swa.swa_hh_scores(x, x, lse, lse.clone(), 1, 4, big),
+              lambda: swa.swa_hh_cache_fill(x, x, lse, k, v, sp, s, big, 1),
+              lambda: swa.swa_hh_cache_fill(x, x, lse, k, v, sp, s, 0, big + 1),
+              lambda: swa.swa_hh_cache_append(x[:, 0], x[:, 0], pos, k, v, sp, s, None, 0, -big + 1),
+              lambda: swa.swa_hh_cache_append(x[:, 0], x[:, 0], pos, k, v, sp, s, None, big, 1),
+              lambda: swa.swa_kv4_cache_append(x[:, 0], x[:, 0], pos, *[torch.zeros(1, 2, 8, 40, device="cuda",
+                                               dtype=torch.uint8) for _ in range(2)], None, None, 8, -big),
+              lambda: swa.swa_rope_axes_qk(x[0], None, pos.expand(1, 4).contiguous(), (big + 32,))):
+        with pytest.raises(ValueError, match="32 bits"):
+            f()
+    scores = []
+    for window in (4, 2 ** 31, big + 1, 2 ** 63 - 1):
+        scores.append(torch.empty(1, 2, 4, device="cuda"))
+        swa.swa_hh_scores(x, x, lse, scores[-1], 4, window, 0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(scores[0], y) for y in scores[1:])
