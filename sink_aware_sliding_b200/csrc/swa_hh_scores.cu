@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                           x.kvh * G + h, x.b * L + t_first + (x.qt_lo + i) * 128);
           }
       }
-      if (*ctl.abort_flag) {  // copies in flight land before the block ends
-        for (int i = max(0, uc - 2); i < uc; ++i) wait_bar(k_full + 8 * (i & 1), (i >> 1) & 1, ctl, false);
-        for (int i = max(0, n - kQStages); i < n; ++i)
-          wait_bar(q_full + 8 * (i % kQStages), (i / kQStages) & 1, ctl, false);
-      }
+      // Copies in flight land before the block ends, whether or not anyone has given up by now: another warp
+      // still may, after this one is through with its list.
+      for (int i = max(0, uc - 2); i < uc; ++i) wait_bar(k_full + 8 * (i & 1), (i >> 1) & 1, ctl, false);
+      for (int i = max(0, n - kQStages); i < n; ++i)
+        wait_bar(q_full + 8 * (i % kQStages), (i / kQStages) & 1, ctl, false);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -209,10 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) tc_commit(k_empty + 8 * kb);
         ++uc;
       }
-      if (*ctl.abort_flag) {  // every product issued is done before TMEM is freed
-        tc_commit(drain);
-        wait_bar(drain, 0, ctl, false);
-      }
+      tc_commit(drain);  // every product issued is done before TMEM is freed, as above
+      wait_bar(drain, 0, ctl, false);
     }
     __syncwarp();
   } else {

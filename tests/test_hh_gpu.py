@@ -427,3 +427,25 @@ def test_integers_that_do_not_fit_32_bits_are_refused():
         swa.swa_hh_scores(x, x, lse, scores[-1], 4, window, 0)
     torch.cuda.synchronize()
     assert all(torch.equal(scores[0], y) for y in scores[1:])
+
+
+@pytest.mark.parametrize("L,n_obs", [(128, 128), (300, 200), (5000, 600)])
+def test_scores_waits_of_a_nanosecond_leave_the_library_usable(L, n_obs):
+    """With a time limit that any wait may exceed, whichever warp gives up first, while others are through with their
+    lists or not: the call ends, reports it or does not, and the next call gives the same bits as ever."""
+    B, H, G, d = 2, 2, 2, 128
+    q, k = rand((B, L, H * G, d), 1).cuda(), rand((B, L, H, d), 2).cuda()
+    lse = torch.empty(B, H * G, L, device="cuda")
+    swa.swa_fwd(q, k, k, torch.empty_like(q), lse, L, 0)
+    want, got = torch.empty(B, H, L, device="cuda"), torch.empty(B, H, L, device="cuda")
+    swa.swa_hh_scores(q, k, lse, want, n_obs, L, 0)
+    assert swa.swa_device_error() == 0
+    for _ in range(5):
+        old = swa.swa_set_wait_timeout_ns(1)
+        try:
+            swa.swa_hh_scores(q, k, lse, got, n_obs, L, 0)
+            assert swa.swa_device_error() in (0, swa.SWA_ERR_DEVICE_TIMEOUT)
+        finally:
+            swa.swa_set_wait_timeout_ns(old)
+        swa.swa_hh_scores(q, k, lse, got, n_obs, L, 0)
+        assert swa.swa_device_error() == 0 and torch.equal(got, want)
