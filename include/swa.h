@@ -383,6 +383,7 @@ int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const 
  *   q [B, L, Hq, d], k [B, L, Hkv, d] bf16, lse [B, Hq, L] float32 as swa_fwd takes and
  *   leaves them (window and n_sink as given there; window >= L for full causal
  *   attention), score [B, Hkv, L] float32 (written whole).  0 <= n_obs <= L.
+ *   An lse from elsewhere may be smaller than the logits: terms above 2^127.5 are infinite.
  * swa_hh_cache_fill: keeps positions of a prompt k, v [B, L, Hkv, d] bf16 given
  *   score_in [B, Hkv, L] float32: all where L <= capacity; else the first n_sink, the
  *   last `recent`, and of the others those with the largest score (of equal ones the

@@ -10,8 +10,12 @@
 // fourth tile keep the exponentials, which bound the kernel (16 a cycle and SM against
 // 4096 multiply-adds: at d = 128 twice the product's time), from waiting for products.
 // Sums: float32 over a tile's 128 columns in four chains, float64 over the tiles.
-// 512 queries on 32768 keys, 32 heads on 8, d = 128 (136 GFLOP, 5.4e8 exponentials): 158 us at
-// 1.96 GHz, 183 us at the 1.7 GHz of the power cap; ex2 alone would take 115 us, the products 82.
+// 512 queries on 32768 keys, 32 heads on 8, d = 128 (136 GFLOP, 5.4e8 exponentials): 162 us at
+// 1.96 GHz (2 us of them for the polynomial's upper bound), 185 us at the 1.7 GHz of the power cap.
+// The products would take 82 us; with three quarters of the exponentials on it ex2 would take 86 us
+// (XU pipe 64% busy, issue slots 56%): what is left are the exponentials' waits for the log-sum-exps,
+// which each thread reads from shared memory through the queue that ex2 uses as well.
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -49,18 +53,17 @@ struct Cfg {
   static constexpr int SMEM = OFF_BAR + 8 * NBAR + 16 + 1024;
 };
 
-// 2^x for two x on the multiply-add pipe, for x of at most about 120: x = n + f with n the nearest integer, a
-// polynomial of degree 5 in f (this build's own fit, minimax in relative error on [-1/2, 1/2]: 2.4e-7 with its
-// float32 rounding), times 2^n.  Below 2^-126 the result is 2^-126; a NaN stays one.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
+// 2^x for two x on the multiply-add pipe: x = n + f with n the nearest integer, a polynomial of degree 5 in f (this
+// build's own fit, minimax in relative error on [-1/2, 1/2]: 2.4e-7 with its float32 rounding), times 2^n.  Below
+// 2^-126 the result is 2^-126, above 2^127.5 infinity (n = 128 has an infinity's bits); a NaN stays one.
+__device__ __forceinline__ float clamp_nan(float x) {
+  asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(-126.f), "f"(128.f));
+  return x;
 }
 __device__ __forceinline__ uint64_t exp2_pair(float x0, float x1) {
   auto both = [](float v) { return f2_pack(v, v); };
   constexpr float kRound = 12582912.f + 127.f;  // 1.5 * 2^23 and the exponent's bias: the sum's low bits are n + 127
-  const uint64_t x = f2_pack(max_nan(x0, -126.f), max_nan(x1, -126.f));
+  const uint64_t x = f2_pack(clamp_nan(x0), clamp_nan(x1));
   const uint64_t r = f2_add(x, both(kRound));
   const uint64_t f = f2_add(x, f2_mul(f2_add(r, both(-kRound)), both(-1.f)));
   uint64_t p = f2_fma(both(0.0013276472454890609f), f, both(0.009675540961325169f));

@@ -449,3 +449,25 @@ def test_scores_waits_of_a_nanosecond_leave_the_library_usable(L, n_obs):
             swa.swa_set_wait_timeout_ns(old)
         swa.swa_hh_scores(q, k, lse, got, n_obs, L, 0)
         assert swa.swa_device_error() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_log_sum_exps_from_elsewhere(d):
+    """Sums too small for the logits (another window, another scale): every column gives 2^x as far as a float goes, and
+    an infinity beyond; a NaN stays one.  One query at a time has weight, on all the ways a column can take."""
+    B, H, L, n_obs = 1, 1, 256, 8
+    q, k = torch.zeros(B, L, H, d).bfloat16().cuda(), rand((B, L, H, d), 1).cuda()
+    for x in (-100.0, 0.0, 100.0, 119.3, 121.0, 125.0, 127.25, 128.25, 130.0, 256.0, 300.5, 1e4, math.inf, math.nan):
+        for t in range(L - n_obs, L):
+            lse = torch.full((B, H, L), 150 * math.log(2), device="cuda")
+            lse[..., t] = -x * math.log(2)
+            score = torch.empty(B, H, L, device="cuda")
+            swa.swa_hh_scores(q, k, lse, score, n_obs, L, 0)
+            got = score[0, 0, :L - n_obs].double().cpu().numpy()
+            # x in the kernel: the float32 log-sum-exp (2^-24 of it) times log2(e), rounded again
+            want = math.nan if x != x else math.inf if x > 128 else 2.0 ** x
+            if x != x or x > 128:
+                np.testing.assert_array_equal(got, want)
+            else:  # and seven columns of 2^-126 at most
+                assert (np.abs(got - want) <= (abs(x) * 2.0 ** -22 + 2.0 ** -20) * want + 8 * 2.0 ** -126).all(), (x, t)
+    assert swa.swa_device_error() == 0
