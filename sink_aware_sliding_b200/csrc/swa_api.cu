@@ -645,7 +645,9 @@ int swa_hh_scores(const void* q, const void* k, const float* lse, float* score, 
     return SWA_ERR_INVALID_ARG;
   const long long T = static_cast<long long>(B) * L;
   const long long units = static_cast<long long>(B) * Hkv * ((L + 127) / 128);
-  if (T > INT32_MAX - 128 || units > INT32_MAX || static_cast<long long>(n_obs) * (Hq / Hkv) > INT32_MAX / 2)
+  // the kernel adds a window of up to L to a key's position, and a grid's blocks to a unit's number
+  if (T > INT32_MAX - 128 || L >= (1 << 30) - 128 || units > INT32_MAX / 2 ||
+      static_cast<long long>(n_obs) * (Hq / Hkv) > INT32_MAX / 2)
     return SWA_ERR_UNSUPPORTED;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != SWA_OK) return st;

@@ -77,6 +77,13 @@ def test_hh_scores(lib, kw, want):
     assert call(lib, "swa_hh_scores", "q k lse sc B Hq Hkv L d n_obs W S scale stream", HH, **kw) == want
 
 
+def test_hh_scores_of_prompts_whose_positions_and_windows_leave_32_bits(lib):
+    order = "q k lse sc B Hq Hkv L d n_obs W S scale stream"
+    for L in (2 ** 30 - 128, 2 ** 30 + 1, 2 ** 31 - 200):
+        assert call(lib, "swa_hh_scores", order, HH, B=1, Hq=1, Hkv=1, d=64, L=L, W=2 ** 31 - 1, n_obs=1) == UNSUP
+    assert call(lib, "swa_hh_scores", order, HH, B=2 ** 28, Hq=8, Hkv=8, d=64, L=1, n_obs=1) == UNSUP
+
+
 CACHE = [(dict(recent=0), BAD), (dict(S=-1), BAD), (dict(S=6), BAD), (dict(C=0), BAD), (dict(C=16385), UNSUP),
          (dict(d=32), UNSUP), (dict(kc=None), BAD), (dict(vc=ODD), BAD), (dict(sp=A + 2), BAD), (dict(sc=None), BAD),
          (dict(B=-1), BAD), (dict(Hkv=0), BAD), (dict(B=0), OK), (dict(B=2 ** 22), UNSUP)]
