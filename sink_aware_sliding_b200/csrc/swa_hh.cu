@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kFillThreads)
   __shared__ unsigned s_warp[kFillWarps];
   __shared__ unsigned s_cut, s_left;
   __shared__ int s_kept[kFillWarps], s_ties[kFillWarps];
-  let_next_kernel_start();  // the copy of the rows; the blocks here are fewer than the SMs where there is one
+  let_next_kernel_start();  // the copy of the rows, if there is one: its blocks come when all blocks here have begun
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const float* in = score_in + static_cast<size_t>(blockIdx.x) * L;
   int32_t* sp = slot_pos + static_cast<size_t>(blockIdx.x) * C;
@@ -325,10 +325,16 @@ cudaError_t launch_hh_fill(const void* k, const void* v, const float* score_in, 
                            cudaStream_t stream) {
   const int segs = B * Hkv;
   const int kept = std::min(L, C), vec = d / 8;
-  // The selecting block copies the rows as well where they are few, which spares the caller a launch (3 us; 128 KB
-  // each of 8 heads: 8.7 us on the GPU against 7.2 us), or where there is a block for most SMs (256 heads: 31.6 against
-  // 36.7 us); else a kernel of its own does (512 KB each of 8 heads: 10.7 us against 20.1 us).
-  const bool here = static_cast<long long>(kept) * vec * 32 <= (132 << 10) || segs >= sms * 7 / 8;
+  // Who copies the rows (K's and V's `bytes` a head): the selecting block itself, which spares the caller a launch,
+  // or a kernel of its own, which has all SMs.  Heads x bytes, microseconds of (itself, own kernel):
+  //   by call   8 x 128 KB 10.3, 11.1   8 x 192 KB 12.3, 11.1   8 x 512 KB 20.6, 11.1   32 x 128 KB 10.3, 11.1
+  //   in a graph 8 x 64 KB 6.8, 6.6     8 x 128 KB 8.3, 6.9    8 x 192 KB 9.9, 7.4     8 x 512 KB 18.6, 9.3
+  // so few rows go with the caller's launch, at 1.4 us of a graph's time at most.  With a block for most SMs
+  // the block itself copies more (in a graph, and by call alike):
+  //   128 x 256 KB 16.6, 17.7   256 x 150 KB 19.3, 21.2   256 x 256 KB 28.7, 29.9   512 x 256 KB 51.3, 56.2
+  //   96 x 512 KB 26.2, 26.0    128 x 512 KB 31.2, 31.2   256 x 512 KB 57.3, 54.6   136 x 1 MB 59.5, 54.3
+  const long long bytes = static_cast<long long>(kept) * vec * 32;
+  const bool here = bytes <= (152 << 10) || (segs >= sms * 7 / 8 && bytes <= (384 << 10));
   const FillRows rows{static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<uint4*>(kc),
                       static_cast<uint4*>(vc), Hkv, vec, kept, here};
   cudaError_t e = cudaSuccess;

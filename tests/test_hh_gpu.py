@@ -471,3 +471,21 @@ def test_scores_of_log_sum_exps_from_elsewhere(d):
             else:  # and seven columns of 2^-126 at most
                 assert (np.abs(got - want) <= (abs(x) * 2.0 ** -22 + 2.0 ** -20) * want + 8 * 2.0 ** -126).all(), (x, t)
     assert swa.swa_device_error() == 0
+
+
+@pytest.mark.parametrize("B,H,L,C,d", [(20, 8, 2500, 1601, 128), (10, 16, 30001, 3203, 64), (32, 8, 3000, 700, 128)])
+def test_fills_of_more_heads_than_the_gpu_takes_at_once(B, H, L, C, d):
+    """A block for every SM and more, few and many rows a head: copied by the choosing block or by a kernel of its own."""
+    S, recent = 4, 100
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn(B, L, H, d, device="cuda", generator=g).bfloat16()
+    s = torch.rand(B, H, L, device="cuda", generator=g)
+    kc, vc = (torch.zeros(B, H, C, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    sp, score = torch.full((B, H, C), L - 1, device="cuda", dtype=torch.int32), torch.zeros(B, H, C, device="cuda")
+    swa.swa_hh_cache_fill(k, -k, s, kc, vc, sp, score, S, recent)
+    at = torch.arange(L, device="cuda")
+    rank = s.masked_fill((at < S) | (at >= L - recent), 2.0)
+    keep = rank.sort(dim=-1, descending=True, stable=True)[1][..., :C].sort(-1)[0]
+    assert torch.equal(sp, keep.int()) and torch.equal(score, s.gather(-1, keep))
+    rows = k.gather(1, keep.transpose(1, 2)[..., None].expand(-1, -1, -1, d)).transpose(1, 2)
+    assert torch.equal(kc, rows) and torch.equal(vc, -rows)
