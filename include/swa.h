@@ -348,7 +348,7 @@ int swa_hadamard_proj(const void* y, const float* alpha, const float* beta, void
  *   to 1.5 * 2^-17 (two bf16 parts), but for products below 2^-73 of the largest step or
  *   minimum of the sequence's rows of V, which may lose bits.  Where a group of V is not
  *   finite, only its own elements of the output are unspecified.
- *   Supported: Hq / Hkv <= 8, |q| < 2^100, step < 2^100.
+ *   Supported: Hq / Hkv <= 8, B <= 4096, |q| < 2^100, step < 2^100.
  */
 size_t swa_kv4_row_bytes(int d);
 int swa_kv4_cache_fill(const void* k, const void* v, int P, void* kcache, void* vcache, void* sink_k, void* sink_v,
@@ -382,7 +382,7 @@ int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const 
  *                      j visible to t:  exp(scale q_t,g . k_j,h - lse[b, g, t]);
  *   q [B, L, Hq, d], k [B, L, Hkv, d] bf16, lse [B, Hq, L] float32 as swa_fwd takes and
  *   leaves them (window and n_sink as given there; window >= L for full causal
- *   attention), score [B, Hkv, L] float32 (written whole).  0 <= n_obs <= L.
+ *   attention), score [B, Hkv, L] float32 (written whole).  0 <= n_obs <= L < 2^30 - 128.
  *   An lse from elsewhere may be smaller than the logits: terms above 2^127.5 are infinite.
  * swa_hh_cache_fill: keeps positions of a prompt k, v [B, L, Hkv, d] bf16 given
  *   score_in [B, Hkv, L] float32: all where L <= capacity; else the first n_sink, the
@@ -401,9 +401,11 @@ int swa_kv4_decode(const void* q, const void* kcache, const void* vcache, const 
  *   or float32 by out_dtype SWA_DTYPE_BF16_F32OUT; lse [B, Hq] float32, may be NULL),
  *   and each occupied slot's score becomes
  *       decay * score + sum over the query heads of the KV head of its softmax weight.
- *   0 <= decay <= 1.  Without occupied slots out = 0, lse = -inf.  Supported:
- *   Hq / Hkv <= 8.  No workspace is needed, so that calls on different caches may run
- *   at once.
+ *   0 <= decay <= 1.  Without occupied slots out = 0, lse = -inf.  Scores and sums are
+ *   float32, the softmax numerators that multiply V two bf16 parts (2^-17 together).
+ *   There are no positions here: the scores of every sequence of the batch change, also of
+ *   one that swa_hh_cache_append left as it is.  Supported: Hq / Hkv <= 8.  No workspace
+ *   is needed, so that calls on different caches may run at once.
  */
 int swa_hh_scores(const void* q, const void* k, const float* lse, float* score, int B, int Hq, int Hkv, int L, int d,
                   int n_obs, int window, int n_sink, float scale, swa_stream_t stream);

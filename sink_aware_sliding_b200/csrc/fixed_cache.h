@@ -7,8 +7,9 @@
 
 namespace swa {
 
-// Division of 0 <= n < 2^31 by a divisor known to the host, in three instructions: with
-// 2^l the power of two at or above d, q = (n + n * mul / 2^32) / 2^l, mul = 2^32 (2^l - d) / d + 1.
+// Division of 0 <= n < 2^31 by a divisor known to the host, in three instructions, as Granlund
+// and Montgomery describe it ("Division by invariant integers using multiplication"): with 2^l
+// the power of two at or above d, q = (n + n * mul / 2^32) / 2^l, mul = 2^32 (2^l - d) / d + 1.
 struct FastDiv {
   uint32_t d, mul, shift;
   explicit FastDiv(int divisor) : d(static_cast<uint32_t>(divisor)), shift(0) {

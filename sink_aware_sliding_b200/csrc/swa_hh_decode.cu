@@ -12,7 +12,7 @@
 // its sums, each block makes weights of its slots' scores and adds them up, without a
 // second pass over K; the scores to add to are read at the block's start.
 // B = 64, 8 KV heads, 4 query heads each, d = 128, 2048 slots (550 MB): 94 us, 5.9 TB/s,
-// 89% of a copy's rate.  With the heads as rows of the products 170 us (one block on an SM),
+// 89% of a copy's rate.  With the heads as rows of the products 180 us (one block on an SM),
 // with the scores read after the loop 106 us, without the L2 policy 96 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

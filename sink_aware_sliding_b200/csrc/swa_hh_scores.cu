@@ -13,8 +13,8 @@
 // 512 queries on 32768 keys, 32 heads on 8, d = 128 (136 GFLOP, 5.4e8 exponentials): 162 us at
 // 1.96 GHz (2 us of them for the polynomial's upper bound), 185 us at the 1.7 GHz of the power cap.
 // The products would take 82 us; with three quarters of the exponentials on it ex2 would take 86 us
-// (XU pipe 64% busy, issue slots 56%): what is left are the exponentials' waits for the log-sum-exps,
-// which each thread reads from shared memory through the queue that ex2 uses as well.
+// (XU pipe 63% busy, issue slots 58%).  What is left is waiting for long loads, over a third of all
+// stalls: tensor memory's, and the next tile's log-sum-exps.
 
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -12,10 +12,11 @@
 // that 1/8 of the code bytes holds four neighbouring elements of every group, which
 // is what one thread of the decode kernel multiplies.
 //
-// Bound by instruction issue (76% of the slots in the fill, ALU pipe 59%): 63 instructions a
-// row.  Four prompts' last 4096 positions and 4 sinks, 8 heads, d = 128 (88 MB each way):
-// fill 21 us, 4.2 TB/s, read 20.5 us; with 16 lanes a row 27 and 23.5 us, with 64-bit
-// divisions for the row's place 41 and 31 us.
+// The fill is bound by instruction issue (76% of the slots, ALU pipe 59%): 63 instructions a row.
+// The read-back waits for loads that depend on each other, position before row (issue 55%, ALU pipe
+// 45%, most of the waiting warps on long loads): 38 instructions a row.  Four prompts' last 4096
+// positions and 4 sinks, 8 heads, d = 128 (88 MB each way): fill 21 us, 4.2 TB/s, read 20.5 us; with
+// 16 lanes a row 27 and 23.5 us, with 64-bit divisions for the row's place 41 and 31 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -237,23 +238,24 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-}  // namespace
-
-namespace {
-// Blocks along x for `units` blocks' worth of work of each of B sequences, k and v: as many
-// as an SM holds at once (`per_sm`), since a block's start costs as much as two of its rows.
-dim3 kv4_grid(long long units, int B, int sms, int per_sm) {
+// Blocks along x for `units` blocks' worth of work of each of B sequences, k and v: 16 blocks of 256 threads for
+// an SM, of which it holds 6 at a time at the 39 registers of d = 128, so that blocks that end early make room for
+// others.  Four prompts' 4100 rows of 8 heads, fill and read-back in microseconds: 6 blocks 22.1 and 19.4, 8 (a
+// second wave of a third) 23.2 and 23.9, 12 21.4 and 19.7, 16 21.1 and 20.3, 24 21.2 and 19.9.
+dim3 kv4_grid(long long units, int B, int sms) {
+  constexpr int kPerSm = 16;
   const int z = std::min(B, 32768);
-  const long long x = std::min(units, std::max(1LL, static_cast<long long>(sms) * per_sm / (2LL * z)));
+  const long long x = std::min(units, std::max(1LL, static_cast<long long>(sms) * kPerSm / (2LL * z)));
   return dim3(static_cast<unsigned>(x), 2, static_cast<unsigned>(z));
 }
+
 }  // namespace
 
 cudaError_t launch_kv4_fill(const void* k, const void* v, int P, void* kc, void* vc, void* sk, void* sv, int B,
                             int Hkv, int d, int W, int S, int sms, cudaStream_t stream) {
   const int n_ring = std::min(P, W);
   const long long rows = static_cast<long long>(Hkv) * (n_ring + std::min(std::min(P, S), P - n_ring));
-  const dim3 grid = kv4_grid((rows + kPer - 1) / kPer, B, sms, 16);
+  const dim3 grid = kv4_grid((rows + kPer - 1) / kPer, B, sms);
   const FastDiv hkv(Hkv);
   auto* c0 = static_cast<uint8_t*>(kc);
   auto* c1 = static_cast<uint8_t*>(vc);
@@ -286,7 +288,7 @@ cudaError_t launch_kv4_append(const void* k, const void* v, const int32_t* pos, 
 cudaError_t launch_kv4_read(const int32_t* positions, int n, const void* kc, const void* vc, const void* sk,
                             const void* sv, void* k_out, void* v_out, bool f32, int B, int Hkv, int d, int W, int S,
                             int sms, cudaStream_t stream) {
-  const dim3 grid = kv4_grid((static_cast<long long>(n) * Hkv + kPer - 1) / kPer, B, sms, 16);
+  const dim3 grid = kv4_grid((static_cast<long long>(n) * Hkv + kPer - 1) / kPer, B, sms);
   const FastDiv hkv(Hkv), w(W);
   const auto* c0 = static_cast<const uint8_t*>(kc);
   const auto* c1 = static_cast<const uint8_t*>(vc);

@@ -27,8 +27,8 @@
 // slots and of the ALU pipe over a launch with its tail), next to HBM.
 // B = 64, 8 KV heads, 4 query heads each, d = 128, window 4096 + 4 sinks (336 MB): 69.3 us,
 // 4.8 TB/s (the copies alone take 53 us); 118 us with the heads as rows and 16 keys a step,
-// 75 us with the keys as rows, 66 us with 32 keys a step and P in fp16.  Under a power cap that
-// lowers the clock to 1.76 GHz it takes 76 us.
+// 75 us with the keys as rows, 66 us with 32 keys a step and P in fp16.  With its append
+// a step takes 74 us by call, 77 us once a longer load has lowered the clock to 1.85 GHz.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -557,3 +557,15 @@ def test_missing_tensors_are_refused_by_name():
         swa.swa_kv4_cache_append(k, k, None, c.kc, c.vc, c.sk, c.sv, 9, 3)
     with pytest.raises(ValueError, match="v_new"):
         swa.swa_kv4_cache_append(k, None, pos, c.kc, c.vc, c.sk, c.sv, 9, 3)
+
+
+@pytest.mark.parametrize("G", [1, 3, 4, 5, 7, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_numerators_keep_sixteen_bits_for_every_number_of_heads(G, d):
+    """Up to four heads the numerators' low parts share a product with the high ones, with more they have their own."""
+    B, H, W = 3, 2, 450
+    k, v = rand((B, H, W, d), 1), rand((B, H, W, d), 2).float()
+    v[..., :32] *= 2.0 ** 25
+    v[:, 1, 100:300] *= 2.0 ** -30
+    c, kq, vq = packed(k, v.bfloat16(), W)
+    check_parts(rand((B, H * G, d), 3, 2.0), c, [W - 1, 31, 200], kq, vq, sixteen_bits)
