@@ -346,8 +346,8 @@ int swa_hadamard_proj(const void* y, const float* alpha, const float* beta, void
  *   at once.  A sequence with pos[b] < 0 has no keys: out = 0, lse = -inf.  Scores and
  *   sums are float32; the softmax numerators, and their products with the steps, are held
  *   to 1.5 * 2^-17 (two bf16 parts), but for products below 2^-73 of the largest step or
- *   minimum of the sequence's rows of V, which may lose bits.  Where a group of V is not
- *   finite, only its own elements of the output are unspecified.
+ *   minimum of the sequence's rows of V (of 2^-40 if that is more), which may lose bits.
+ *   Where a group of V is not finite, only its own elements of the output are unspecified.
  *   Supported: Hq / Hkv <= 8, B <= 4096, |q| < 2^100, step < 2^100.
  */
 size_t swa_kv4_row_bytes(int d);
