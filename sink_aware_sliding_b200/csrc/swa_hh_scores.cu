@@ -53,8 +53,8 @@ struct Cfg {
   static constexpr int SMEM = OFF_BAR + 8 * NBAR + 16 + 1024;
 };
 
-// 2^x for two x on the multiply-add pipe: x = n + f with n the nearest integer, a polynomial of degree 5 in f (this
-// build's own fit, minimax in relative error on [-1/2, 1/2]: 2.4e-7 with its float32 rounding), times 2^n.  Below
+// 2^x for two x on the multiply-add pipe: x = n + f with n the nearest integer, a polynomial of degree 5 in f (a
+// fit of its own, minimax in relative error on [-1/2, 1/2]: 2.4e-7 with its float32 rounding), times 2^n.  Below
 // 2^-126 the result is 2^-126, above 2^127.5 infinity (n = 128 has an infinity's bits); a NaN stays one.
 __device__ __forceinline__ float clamp_nan(float x) {
   asm("max.NaN.f32 %0, %0, %1;\n\tmin.NaN.f32 %0, %0, %2;" : "+f"(x) : "f"(-126.f), "f"(128.f));
